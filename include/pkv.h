@@ -34,16 +34,19 @@
  *   - Supported: block_size 16; head_dim 64 or 128; num_q_heads a multiple of
  *     num_kv_heads; dtype PKV_F32 or PKV_BF16 (same dtype for Q, K, V and
  *     the output), or an 8-bit E4M3 cache with bf16 Q and output through the
- *     _e4m3 entry points.  Arithmetic is fp32 with fp32 accumulation (the
+ *     _e4m3 entry points, or a 4-bit E2M1 cache of pages (pkv_write_e2m1)
+ *     through the _e2m1 ones.  Arithmetic is fp32 with fp32 accumulation (the
  *     tensor-core prefill rounds P to bf16 for its P.V product).
  *
- * Entry points: pkv_write / pkv_write_e4m3 (slot-mapped write), pkv_stage_inputs
+ * Entry points: pkv_write / pkv_write_e4m3 / pkv_write_e2m1 (slot-mapped write),
+ * pkv_read_e2m1 (cached rows read back), pkv_stage_inputs
  * (a step's packed inputs copied to the device), pkv_num_splits
- * and pkv_workspace_bytes (split-KV sizing), pkv_attention_varlen and its
- * variants _window (sliding window), _e4m3 (8-bit cache), _e4m3_window and
- * _noalloc (no caller workspace), pkv_write_attention_varlen / _e4m3 (write
- * and attend in one call, the write folded into the decode kernel for decode
- * steps), pkv_cascade_splits / pkv_cascade_workspace_bytes /
+ * / pkv_num_splits_e2m1 and pkv_workspace_bytes (split-KV sizing),
+ * pkv_attention_varlen and its variants _window (sliding window), _e4m3 (8-bit
+ * cache), _e4m3_window, _e2m1 (4-bit cache) and _noalloc (no caller
+ * workspace), pkv_write_attention_varlen / _e4m3 / _e2m1 (write and attend in
+ * one call, the write folded into the decode kernel for decode steps over all
+ * but E2M1 caches), pkv_cascade_splits / pkv_cascade_workspace_bytes /
  * pkv_cascade_attention / _e4m3 (requests sharing a block-aligned prefix),
  * pkv_build_metadata (the step's flat-batch metadata, host only) and
  * pkv_status_string.
@@ -133,6 +136,57 @@ pkv_status pkv_write_e4m3(const void* k_new, const void* v_new, const int64_t* s
                           float k_scale, float v_scale, int32_t* error_flag, void* stream);
 
 /*
+ * pkv_write_e2m1 - pkv_write into a 4-bit E2M1 cache.
+ *
+ * "Model execution", section "Where it breaks": quantised KV caches are a
+ * backend feature; the pages fix no 4-bit format.  This library's: a stored
+ * element stands for t * value(s) * value(c), with t the cache tensor's fp32
+ * scale (k_scale or v_scale), s an E4M3 code for 16 consecutive elements of a
+ * token's head row, and c an E2M1 code (sign, 2 exponent bits with bias 1, 1
+ * mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6).  For 16 elements x:
+ *   y = x / t,  s = E4M3(max |y| / 6),  c = E2M1(y / value(s)),
+ * every division correctly rounded in fp32, every code the nearest one (ties
+ * to even) with magnitudes beyond the largest (448 and 6) saturating; s = 0
+ * gives codes 0, and a NaN among the 16 gives s the NaN code and codes 0.
+ *
+ * Each cache is [num_blocks, num_kv_heads, 9 * head_dim] bytes.  The page of one
+ * (block, KV head) holds its 16 tokens' rows of head_dim / 2 code bytes (element
+ * 2 i in the low nibble of byte i, 2 i + 1 in the high one), then its 16 tokens'
+ * rows of head_dim / 16 scale bytes: 4.5 bits an element.
+ *
+ *   k_new, v_new   device, [num_tokens, num_kv_heads, head_dim], src_dtype
+ *                  (PKV_F32 or PKV_BF16).
+ *   k_cache, v_cache  device, as above, 16-byte aligned.
+ *   k_scale, v_scale  finite, > 0.
+ *   head_dim 64 or 128 (else PKV_ERR_UNSUPPORTED).  slot_mapping, error_flag and
+ *   the rest as pkv_write; two tokens naming the same slot leave its contents
+ *   unspecified (codes and scales may be of different tokens).
+ */
+pkv_status pkv_write_e2m1(const void* k_new, const void* v_new, const int64_t* slot_mapping,
+                          int64_t num_tokens, void* k_cache, void* v_cache, int64_t num_blocks,
+                          int block_size, int num_kv_heads, int head_dim, pkv_dtype src_dtype,
+                          float k_scale, float v_scale, int32_t* error_flag, void* stream);
+
+/*
+ * pkv_read_e2m1 - the rows at the given slots of an E2M1 cache, widened.
+ *
+ * The inverse of pkv_write_e2m1, for moving a request's context to another
+ * cache or engine: row i of k_out (v_out) becomes the values of slot
+ * slot_mapping[i], t * (value(s) * value(c)) rounded to fp32 and then to
+ * out_dtype.  A slot may be named any number of times.
+ *   slot_mapping   device int64 [num_rows]; rows with a negative slot keep
+ *                  their contents, and so do rows with a slot >= num_blocks *
+ *                  block_size, flagged PKV_FLAG_BAD_SLOT.
+ *   k_out, v_out   device, [num_rows, num_kv_heads, head_dim], out_dtype
+ *                  (PKV_F32 or PKV_BF16); not overlapping the caches.
+ *   The rest as pkv_write_e2m1.  num_rows == 0 is a no-op returning PKV_OK.
+ */
+pkv_status pkv_read_e2m1(const void* k_cache, const void* v_cache, const int64_t* slot_mapping,
+                         int64_t num_rows, void* k_out, void* v_out, int64_t num_blocks,
+                         int block_size, int num_kv_heads, int head_dim, pkv_dtype out_dtype,
+                         float k_scale, float v_scale, int32_t* error_flag, void* stream);
+
+/*
  * pkv_stage_inputs - copy a step's packed inputs into device memory.
  *
  * "Inside the engine: kernels, CUDA graphs and the life of a request",
@@ -172,6 +226,13 @@ pkv_status pkv_stage_inputs(void* dst, const void* src, int64_t nbytes, void* st
  */
 int pkv_num_splits(int num_seqs, int max_query_len, int max_seq_len, int num_q_heads,
                    int num_kv_heads, int head_dim, int device);
+
+/*
+ * pkv_num_splits_e2m1 - the same for pkv_attention_varlen_e2m1: its own count,
+ * as its tiles hold 8 or 16 rows.  The same bounds.
+ */
+int pkv_num_splits_e2m1(int num_seqs, int max_query_len, int max_seq_len, int num_q_heads,
+                        int num_kv_heads, int head_dim, int device);
 
 /*
  * pkv_workspace_bytes - device workspace pkv_attention_varlen needs.
@@ -357,6 +418,55 @@ pkv_status pkv_write_attention_varlen_e4m3(
     int64_t num_tokens, int max_query_len, int max_seq_len, int num_q_heads, int num_kv_heads,
     int head_dim, int block_size, float softmax_scale, float k_scale, float v_scale, int causal,
     int num_splits, void* workspace, size_t workspace_bytes, int32_t* error_flag,
+    int64_t num_blocks, void* stream);
+
+/*
+ * pkv_attention_varlen_e2m1 - pkv_attention_varlen over an E2M1 cache.
+ *
+ * The cache format of pkv_write_e2m1; with K and V the products value(s) *
+ * value(c) of key j,
+ *   out[t, h, :] = v_scale * sum_j softmax_j(softmax_scale * k_scale *
+ *                  q[t,h,:] . K_j) V_j
+ * (lse_out: the natural-log log-sum-exp of those scaled scores).  The products
+ * are widened exactly to f16; each q row enters as f16 scaled by a power of two
+ * (its largest magnitude in [2^14, 2^15): exact for every element within 2^31
+ * of it); both contractions run on tensor cores with fp32 accumulation, P
+ * rounded to f16 for P.V.
+ *   q, out            device bf16 [num_tokens, num_q_heads, head_dim].
+ *   k_cache, v_cache  device, [num_blocks, num_kv_heads, 9 * head_dim] bytes.
+ *   k_scale, v_scale  finite, > 0 (else PKV_ERR_INVALID_ARG).
+ *   window            0: none; > 0: the row at position p keeps keys j with
+ *                     p - window < j, on top of the causal limit, as
+ *                     pkv_attention_varlen_window; < 0: PKV_ERR_INVALID_ARG.
+ *   num_splits        0 = pkv_num_splits_e2m1(...) (with a window, for a context
+ *                     of window + PKV_DECODE_MAX_QLEN keys); else 1..64.
+ * What cache slots hold that a row may not see (behind a context, after its
+ * position, before its window) never reaches the row, NaN scales included.
+ * Everything else as pkv_attention_varlen, workspace included.
+ */
+pkv_status pkv_attention_varlen_e2m1(const void* q, const void* k_cache, const void* v_cache,
+                                     void* out, float* lse_out, const int32_t* query_start_loc,
+                                     const int32_t* seq_lens, const int32_t* block_table,
+                                     int max_blocks_per_seq, int num_seqs, int64_t num_tokens,
+                                     int max_query_len, int max_seq_len, int num_q_heads,
+                                     int num_kv_heads, int head_dim, int block_size,
+                                     float softmax_scale, float k_scale, float v_scale, int causal,
+                                     int window, int num_splits, void* workspace,
+                                     size_t workspace_bytes, int32_t* error_flag,
+                                     int64_t num_blocks, void* stream);
+
+/*
+ * pkv_write_attention_varlen_e2m1 - pkv_write_e2m1 (bf16 rows) then
+ * pkv_attention_varlen_e2m1, as one call: every argument is checked before
+ * anything is enqueued.  All num_tokens rows are stored at their slots.
+ */
+pkv_status pkv_write_attention_varlen_e2m1(
+    const void* k_new, const void* v_new, const int64_t* slot_mapping, const void* q,
+    void* k_cache, void* v_cache, void* out, float* lse_out, const int32_t* query_start_loc,
+    const int32_t* seq_lens, const int32_t* block_table, int max_blocks_per_seq, int num_seqs,
+    int64_t num_tokens, int max_query_len, int max_seq_len, int num_q_heads, int num_kv_heads,
+    int head_dim, int block_size, float softmax_scale, float k_scale, float v_scale, int causal,
+    int window, int num_splits, void* workspace, size_t workspace_bytes, int32_t* error_flag,
     int64_t num_blocks, void* stream);
 
 /*

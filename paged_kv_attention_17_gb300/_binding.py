@@ -27,7 +27,9 @@ EXPORTS = ("pkv_write", "pkv_write_e4m3", "pkv_stage_inputs", "pkv_num_splits", 
            "pkv_attention_varlen_e4m3", "pkv_write_attention_varlen_e4m3",
            "pkv_attention_varlen_e4m3_window", "pkv_cascade_attention_e4m3",
            "pkv_attention_varlen_noalloc", "pkv_cascade_splits", "pkv_cascade_workspace_bytes",
-           "pkv_cascade_attention", "pkv_build_metadata", "pkv_status_string")
+           "pkv_cascade_attention", "pkv_build_metadata", "pkv_status_string",
+           "pkv_write_e2m1", "pkv_read_e2m1", "pkv_num_splits_e2m1", "pkv_attention_varlen_e2m1",
+           "pkv_write_attention_varlen_e2m1")
 
 
 class PkvError(RuntimeError):
@@ -101,6 +103,23 @@ def lib() -> ctypes.CDLL:
         L.pkv_build_metadata.argtypes = [i32, vp, vp, vp, vp, i32, i32, i64, vp, vp, vp, vp, vp,
                                          vp, vp]
         L.pkv_build_metadata.restype = i32
+        L.pkv_write_e2m1.argtypes = [vp, vp, vp, i64, vp, vp, i64, i32, i32, i32, i32, f32, f32,
+                                     vp, vp]
+        L.pkv_write_e2m1.restype = i32
+        L.pkv_read_e2m1.argtypes = [vp, vp, vp, i64, vp, vp, i64, i32, i32, i32, i32, f32, f32,
+                                    vp, vp]
+        L.pkv_read_e2m1.restype = i32
+        L.pkv_num_splits_e2m1.argtypes = [i32] * 7
+        L.pkv_num_splits_e2m1.restype = i32
+        L.pkv_attention_varlen_e2m1.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i64, i32,
+                                                i32, i32, i32, i32, i32, f32, f32, f32, i32, i32,
+                                                i32, vp, sz, vp, i64, vp]
+        L.pkv_attention_varlen_e2m1.restype = i32
+        L.pkv_write_attention_varlen_e2m1.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
+                                                      i32, i32, i64, i32, i32, i32, i32, i32, i32,
+                                                      f32, f32, f32, i32, i32, i32, vp, sz, vp,
+                                                      i64, vp]
+        L.pkv_write_attention_varlen_e2m1.restype = i32
         L.pkv_status_string.argtypes = [i32]
         L.pkv_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -418,6 +437,163 @@ def pkv_cascade_attention(q, k_cache, v_cache, out, query_start_loc, suffix_lens
         float(softmax_scale), splits, _ptr(workspace), int(ws_bytes), _ptr(error_flag), int(nb),
         _dtype_code(q.dtype), _stream(stream))
     _check("pkv_cascade_attention", code)
+    return out
+
+
+def _need(device, **tensors):
+    """Each named (tensor, dtype, shape) is a contiguous CUDA tensor of that
+    dtype and shape on the device; an entry whose tensor is None is skipped."""
+    for name, (t, dtype, shape) in tensors.items():
+        if t is None:
+            continue
+        if t.dtype != dtype:
+            raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _e2m1_dims(k_cache):
+    """(device, num_blocks, num_kv_heads, head_dim) of a cache of E2M1 pages."""
+    device = k_cache.device
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"the caches are on {device}, not on the current CUDA device")
+    if k_cache.dim() != 3 or k_cache.shape[2] % 9:
+        raise ValueError("an E2M1 cache is [num_blocks, num_kv_heads, 9 * head_dim]")
+    nb, hkv, page = k_cache.shape
+    return device, nb, hkv, page // 9
+
+
+def pkv_write_e2m1(k_new, v_new, slot_mapping, k_cache, v_cache, k_scale, v_scale,
+                   error_flag=None, stream=None):
+    """pkv_write into 4-bit E2M1 caches (uint8 [num_blocks, Hkv, 9 D]: codes and
+    block scales): slot slot_mapping[t] gets k_new[t] / k_scale and
+    v_new[t] / v_scale, quantised (inputs [N, Hkv, D], fp32 or bf16)."""
+    dev, nb, hkv, d = _e2m1_dims(k_cache)
+    src = _dtype_code(k_new.dtype)
+    n = slot_mapping.numel()
+    rows = (n, hkv, d)
+    _need(dev, k_new=(k_new, k_new.dtype, rows), v_new=(v_new, k_new.dtype, rows),
+          slot_mapping=(slot_mapping, torch.int64, (n,)),
+          k_cache=(k_cache, torch.uint8, k_cache.shape),
+          v_cache=(v_cache, torch.uint8, k_cache.shape),
+          error_flag=(error_flag, torch.int32, (1,)))
+    _check("pkv_write_e2m1", lib().pkv_write_e2m1(
+        k_new.data_ptr(), v_new.data_ptr(), slot_mapping.data_ptr(), n, k_cache.data_ptr(),
+        v_cache.data_ptr(), nb, 16, hkv, d, src, float(k_scale), float(v_scale),
+        _ptr(error_flag), _stream(stream)))
+
+
+def pkv_read_e2m1(k_cache, v_cache, slot_mapping, k_out, v_out, k_scale, v_scale,
+                  error_flag=None, stream=None):
+    """The values at slots slot_mapping of E2M1 caches into k_out / v_out
+    ([N, Hkv, D], fp32 or bf16); rows with a negative slot keep theirs."""
+    dev, nb, hkv, d = _e2m1_dims(k_cache)
+    out = _dtype_code(k_out.dtype)
+    n = slot_mapping.numel()
+    rows = (n, hkv, d)
+    _need(dev, k_out=(k_out, k_out.dtype, rows), v_out=(v_out, k_out.dtype, rows),
+          slot_mapping=(slot_mapping, torch.int64, (n,)),
+          k_cache=(k_cache, torch.uint8, k_cache.shape),
+          v_cache=(v_cache, torch.uint8, k_cache.shape),
+          error_flag=(error_flag, torch.int32, (1,)))
+    _check("pkv_read_e2m1", lib().pkv_read_e2m1(
+        k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), n, k_out.data_ptr(),
+        v_out.data_ptr(), nb, 16, hkv, d, out, float(k_scale), float(v_scale), _ptr(error_flag),
+        _stream(stream)))
+    return k_out, v_out
+
+
+def pkv_num_splits_e2m1(num_seqs, max_query_len, max_seq_len, num_q_heads, num_kv_heads, head_dim,
+                        device=None) -> int:
+    dev = torch.cuda.current_device() if device is None else int(device)
+    return int(lib().pkv_num_splits_e2m1(int(num_seqs), int(max_query_len), int(max_seq_len),
+                                         int(num_q_heads), int(num_kv_heads), int(head_dim), dev))
+
+
+def _e2m1_batch(q, k_cache, v_cache, out, query_start_loc, seq_lens, block_table, max_query_len,
+                max_seq_len, num_splits, workspace, lse_out, error_flag, window):
+    """Checks of the attention's tensors; the call's dimensions, its split count
+    and its workspace.  A given workspace is passed on with the given count (0:
+    the library's own); without one, it is allocated here when needed."""
+    dev, nb, hkv, d = _e2m1_dims(k_cache)
+    if q.dim() != 3 or q.shape[2] != d:
+        raise ValueError(f"q is [num_tokens, Hq, {d}] for these caches")
+    n_tok, hq, _ = q.shape
+    seqs = seq_lens.numel()
+    if block_table.dim() != 2:
+        raise ValueError("block_table is [num_seqs, max_blocks_per_seq]")
+    width = block_table.shape[1]
+    i32 = torch.int32
+    _need(dev, q=(q, torch.bfloat16, q.shape), k_cache=(k_cache, torch.uint8, k_cache.shape),
+          v_cache=(v_cache, torch.uint8, k_cache.shape),
+          query_start_loc=(query_start_loc, i32, (seqs + 1,)), seq_lens=(seq_lens, i32, (seqs,)),
+          block_table=(block_table, i32, (seqs, width)),
+          lse_out=(lse_out, torch.float32, (n_tok, hq)), error_flag=(error_flag, i32, (1,)))
+    # (the graph runner's rows lie in pinned host memory that the device addresses)
+    if out.is_cuda or not out.is_pinned():
+        _need(dev, out=(out, torch.bfloat16, q.shape))
+    elif out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous():
+        raise ValueError("out is bf16, contiguous and of q's shape")
+    splits, ws_bytes = int(num_splits), 0
+    if workspace is None:
+        if splits == 0 and seqs > 0:
+            splits = pkv_num_splits_e2m1(seqs, max_query_len, split_span(max_seq_len, window), hq,
+                                         hkv, d, dev.index)
+        ws_bytes = pkv_workspace_bytes(seqs, hq, d, splits)
+        if ws_bytes:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    else:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError("workspace is a contiguous tensor on the caches' device")
+        ws_bytes = workspace.numel() * workspace.element_size()
+    return (width, seqs, n_tok, int(max_query_len), int(max_seq_len), hq, hkv, d, 16, nb, splits,
+            workspace, ws_bytes)
+
+
+def pkv_attention_varlen_e2m1(q, k_cache, v_cache, out, query_start_loc, seq_lens, block_table,
+                              max_query_len, max_seq_len, softmax_scale, k_scale, v_scale,
+                              causal=True, num_splits=0, workspace=None, lse_out=None,
+                              error_flag=None, stream=None, window=0):
+    """pkv_attention_varlen over uint8 caches [num_blocks, Hkv, 9 D] of E2M1
+    codes and block scales; q and out are bf16.  ``window`` > 0: the row at
+    position p sees keys j > p - window only.  ``workspace`` as for
+    pkv_attention_varlen (sized with pkv_num_splits_e2m1)."""
+    (width, seqs, n_tok, mq, ms, hq, hkv, d, bs, nb, splits, workspace, ws_bytes) = _e2m1_batch(
+        q, k_cache, v_cache, out, query_start_loc, seq_lens, block_table, max_query_len,
+        max_seq_len, num_splits, workspace, lse_out, error_flag, window)
+    _check("pkv_attention_varlen_e2m1", lib().pkv_attention_varlen_e2m1(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), _ptr(lse_out),
+        query_start_loc.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), width, seqs,
+        n_tok, mq, ms, hq, hkv, d, bs, float(softmax_scale), float(k_scale), float(v_scale),
+        1 if causal else 0, int(window), splits, _ptr(workspace), ws_bytes, _ptr(error_flag), nb,
+        _stream(stream)))
+    return out
+
+
+def pkv_write_attention_varlen_e2m1(k_new, v_new, slot_mapping, q, k_cache, v_cache, out,
+                                    query_start_loc, seq_lens, block_table, max_query_len,
+                                    max_seq_len, softmax_scale, k_scale, v_scale, causal=True,
+                                    num_splits=0, workspace=None, lse_out=None, error_flag=None,
+                                    stream=None, window=0):
+    """pkv_write_e2m1 of the bf16 k_new / v_new, then pkv_attention_varlen_e2m1,
+    in one call."""
+    (width, seqs, n_tok, mq, ms, hq, hkv, d, bs, nb, splits, workspace, ws_bytes) = _e2m1_batch(
+        q, k_cache, v_cache, out, query_start_loc, seq_lens, block_table, max_query_len,
+        max_seq_len, num_splits, workspace, lse_out, error_flag, window)
+    rows = (n_tok, hkv, d)
+    _need(q.device, k_new=(k_new, torch.bfloat16, rows), v_new=(v_new, torch.bfloat16, rows),
+          slot_mapping=(slot_mapping, torch.int64, (n_tok,)))
+    _check("pkv_write_attention_varlen_e2m1", lib().pkv_write_attention_varlen_e2m1(
+        k_new.data_ptr(), v_new.data_ptr(), slot_mapping.data_ptr(), q.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), _ptr(lse_out),
+        query_start_loc.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), width, seqs,
+        n_tok, mq, ms, hq, hkv, d, bs, float(softmax_scale), float(k_scale), float(v_scale),
+        1 if causal else 0, int(window), splits, _ptr(workspace), ws_bytes, _ptr(error_flag), nb,
+        _stream(stream)))
     return out
 
 

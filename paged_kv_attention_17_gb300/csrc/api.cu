@@ -19,6 +19,18 @@ cudaError_t launch_kv_write_e4m3(const void* k_new, const void* v_new, bool src_
                                  void* v_cache, int64_t num_slots, uint32_t row_elems,
                                  float k_scale, float v_scale, int32_t* flag, int num_sms,
                                  cudaStream_t stream);
+cudaError_t launch_kv_write_e2m1(const void* k_new, const void* v_new, bool src_bf16,
+                                 const int64_t* slots, int64_t num_tokens, void* k_cache,
+                                 void* v_cache, int64_t num_slots, int hkv, int head_dim,
+                                 float k_scale, float v_scale, int32_t* flag, int num_sms,
+                                 cudaStream_t stream);
+cudaError_t launch_kv_read_e2m1(const void* k_cache, const void* v_cache, const int64_t* slots,
+                                int64_t num_rows, void* k_out, void* v_out, bool out_bf16,
+                                int64_t num_slots, int hkv, int head_dim, float k_scale,
+                                float v_scale, int32_t* flag, int num_sms, cudaStream_t stream);
+cudaError_t launch_decode_e2m1(const AttnArgs& a, int head_dim, cudaStream_t stream);
+int decode_e2m1_rows_per_tile(int group, int max_query_len, bool long_rows);
+int decode_e2m1_ctas_per_sm(int rows_per_tile);
 cudaError_t launch_decode(const AttnArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
                           ElemType et, int head_dim, bool pdl, cudaStream_t stream);
 cudaError_t launch_combine(const AttnArgs& a, ElemType et, int head_dim, cudaStream_t stream);
@@ -183,13 +195,17 @@ int split_rule(int num_seqs, int max_query_len, int max_seq_len, int num_q_heads
   if (sms <= 0) return 0;
   const int group = num_q_heads / num_kv_heads;
   const int qd = max_query_len < kDecodeMaxQ ? (max_query_len < 1 ? 1 : max_query_len) : kDecodeMaxQ;
-  const int R = decode_rows_per_tile(group, qd, false);
+  const bool e2m1 = et == ElemType::kE2m1;
+  const int R = e2m1 ? decode_e2m1_rows_per_tile(group, qd, false)
+                     : decode_rows_per_tile(group, qd, false);
   const int64_t units = static_cast<int64_t>(num_seqs) * num_kv_heads * ((group * qd + R - 1) / R);
   // decode CTA slots of the device (two per SM for the tensor-core build);
   // 7/8 of them leave room for the combine and the next launch's prologue
   // (decode at context 8192, 8 KV heads, bf16, 152 SMs: 16 splits take
   // 14 us a call, 32 splits 10.8 us; a second wave at 40 splits 18 us)
-  const int64_t capacity = static_cast<int64_t>(sms) * decode_ctas_per_sm(et, head_dim);
+  const int64_t capacity =
+      static_cast<int64_t>(sms) *
+      (e2m1 ? decode_e2m1_ctas_per_sm(R) : decode_ctas_per_sm(et, head_dim));
   const int64_t target = capacity * 7 / 8;
   int64_t s = target / units;
   if (s <= 1) return 1;
@@ -287,9 +303,10 @@ static pkv_status attention(const void* q, const void* k_cache, const void* v_ca
   // have outputs large enough for its bf16 P rounding to show.
   const bool tc_prefill = prefill_supported(head_dim, et, num_q_heads / num_kv_heads) &&
                           softmax_scale > 0.f && (window == 0 || window >= kTcMinWindow);
-  // E4M3 caches: decode rows take the register-q tiles, longer requests the
-  // CUDA-core tiles of the same kernel
-  a.long_rows = tc_prefill ? 0 : (et == ElemType::kE4m3 ? (max_query_len > kDecodeMaxQ) : 1);
+  // E4M3 and E2M1 caches: decode rows take their own tiles (register-q, E2M1
+  // tiles of 8 or 16 rows), longer requests the wide tiles of the same kernel
+  const bool codes = et == ElemType::kE4m3 || et == ElemType::kE2m1;
+  a.long_rows = tc_prefill ? 0 : (codes ? (max_query_len > kDecodeMaxQ) : 1);
   if (need > 0) {
     const size_t rows = static_cast<size_t>(splits) * num_seqs * kDecodeMaxQ * num_q_heads;
     a.ws_o = static_cast<float*>(workspace);
@@ -300,7 +317,7 @@ static pkv_status attention(const void* q, const void* k_cache, const void* v_ca
   a.num_blocks = num_blocks;
   a.k_cache = k_cache;
   a.v_cache = v_cache;
-  if (fuse_slots != nullptr) {
+  if (fuse_slots != nullptr && et != ElemType::kE2m1) {
     // the step's new K/V are stored by the decode kernel (every request is
     // decode-class, checked by the caller)
     a.fuse_write = 1;
@@ -313,7 +330,8 @@ static pkv_status attention(const void* q, const void* k_cache, const void* v_ca
 
   // the decode kernel's maps (the tensor-core prefill encodes its own below)
   CUtensorMap kmap, vmap;
-  if (!encode_decode_maps(&kmap, &vmap, k_cache, v_cache, num_slots, num_kv_heads, head_dim, et))
+  if (et != ElemType::kE2m1 &&
+      !encode_decode_maps(&kmap, &vmap, k_cache, v_cache, num_slots, num_kv_heads, head_dim, et))
     return PKV_ERR_CUDA;
 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -322,7 +340,20 @@ static pkv_status attention(const void* q, const void* k_cache, const void* v_ca
   // started, which the long CTAs first would delay
   const bool prefill_follows = tc_prefill && max_query_len > kDecodeMaxQ;
   a.lpt = splits == 1 && num_seqs >= 2 && num_seqs <= kLptMaxSeqs && !prefill_follows ? 1 : 0;
-  cudaError_t e = launch_decode(a, kmap, vmap, et, head_dim, /*pdl=*/true, st);
+  cudaError_t e = cudaSuccess;
+  if (et == ElemType::kE2m1) {
+    // (the write is a launch of its own: a block's scale needs 16 elements)
+    if (fuse_slots != nullptr) {
+      const int sms = current_sms();
+      if (sms <= 0) return PKV_ERR_CUDA;
+      e = launch_kv_write_e2m1(fuse_k_new, fuse_v_new, true, fuse_slots, num_tokens,
+                               const_cast<void*>(k_cache), const_cast<void*>(v_cache), num_slots,
+                               num_kv_heads, head_dim, k_scale, v_scale, error_flag, sms, st);
+    }
+    if (e == cudaSuccess) e = launch_decode_e2m1(a, head_dim, st);
+  } else {
+    e = launch_decode(a, kmap, vmap, et, head_dim, /*pdl=*/true, st);
+  }
   if (e == cudaSuccess && splits > 1) e = launch_combine(a, et, head_dim, st);
   if (e == cudaSuccess && tc_prefill && max_query_len > kDecodeMaxQ) {
     CUtensorMap qmap, kmap_sw, vmap_sw;
@@ -345,6 +376,31 @@ static pkv_status attention(const void* q, const void* k_cache, const void* v_ca
 }
 
 }  // namespace
+
+// The checks that the write into and the read from an E2M1 cache share; rows
+// and cache are the call's row tensors and caches, in either direction.
+template <typename Launch>
+static pkv_status e2m1_rows(const void* k_rows, const void* v_rows, const int64_t* slot_mapping,
+                            int64_t num_rows, const void* k_cache, const void* v_cache,
+                            int64_t num_blocks, int block_size, int num_kv_heads, int head_dim,
+                            pkv_dtype dtype, float k_scale, float v_scale,
+                            const int32_t* error_flag, Launch launch) {
+  if (num_rows < 0 || num_blocks < 1 || num_kv_heads < 1 || head_dim < 1 || !valid_dtype(dtype) ||
+      !valid_scale(k_scale) || !valid_scale(v_scale))
+    return PKV_ERR_INVALID_ARG;
+  if (block_size != kBlock || (head_dim != 64 && head_dim != 128)) return PKV_ERR_UNSUPPORTED;
+  if (num_rows == 0) return PKV_OK;
+  if (!k_rows || !v_rows || !slot_mapping || !k_cache || !v_cache) return PKV_ERR_INVALID_ARG;
+  if (!aligned(k_rows, 16) || !aligned(v_rows, 16) || !aligned(k_cache, 16) ||
+      !aligned(v_cache, 16) || !aligned(slot_mapping, 8) ||
+      (error_flag && !aligned(error_flag, 4)))
+    return PKV_ERR_INVALID_ARG;
+  const int sms = current_sms();
+  if (sms <= 0) return PKV_ERR_CUDA;
+  if (launch(sms) == cudaSuccess) return PKV_OK;
+  cudaGetLastError();
+  return PKV_ERR_CUDA;
+}
 
 // The prefix split count: splits of at least four whole 128-key tiles over
 // the tensor-core prefix pass's 256-row tiles (tc), or of >= 8 blocks over
@@ -443,6 +499,39 @@ pkv_status pkv_write_e4m3(const void* k_new, const void* v_new, const int64_t* s
                                        static_cast<uint32_t>(row_elems), k_scale, v_scale,
                                        error_flag, sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+pkv_status pkv_write_e2m1(const void* k_new, const void* v_new, const int64_t* slot_mapping,
+                          int64_t num_tokens, void* k_cache, void* v_cache, int64_t num_blocks,
+                          int block_size, int num_kv_heads, int head_dim, pkv_dtype src_dtype,
+                          float k_scale, float v_scale, int32_t* error_flag, void* stream) {
+  return e2m1_rows(k_new, v_new, slot_mapping, num_tokens, k_cache, v_cache, num_blocks,
+                   block_size, num_kv_heads, head_dim, src_dtype, k_scale, v_scale, error_flag,
+                   [&](int sms) {
+                     return launch_kv_write_e2m1(
+                         k_new, v_new, src_dtype == PKV_BF16, slot_mapping, num_tokens, k_cache,
+                         v_cache, num_blocks * kBlock, num_kv_heads, head_dim, k_scale, v_scale,
+                         error_flag, sms, static_cast<cudaStream_t>(stream));
+                   });
+}
+
+pkv_status pkv_read_e2m1(const void* k_cache, const void* v_cache, const int64_t* slot_mapping,
+                         int64_t num_rows, void* k_out, void* v_out, int64_t num_blocks,
+                         int block_size, int num_kv_heads, int head_dim, pkv_dtype out_dtype,
+                         float k_scale, float v_scale, int32_t* error_flag, void* stream) {
+  return e2m1_rows(k_out, v_out, slot_mapping, num_rows, k_cache, v_cache, num_blocks, block_size,
+                   num_kv_heads, head_dim, out_dtype, k_scale, v_scale, error_flag, [&](int sms) {
+                     return launch_kv_read_e2m1(
+                         k_cache, v_cache, slot_mapping, num_rows, k_out, v_out,
+                         out_dtype == PKV_BF16, num_blocks * kBlock, num_kv_heads, head_dim,
+                         k_scale, v_scale, error_flag, sms, static_cast<cudaStream_t>(stream));
+                   });
+}
+
+int pkv_num_splits_e2m1(int num_seqs, int max_query_len, int max_seq_len, int num_q_heads,
+                        int num_kv_heads, int head_dim, int device) {
+  return split_rule(num_seqs, max_query_len, max_seq_len, num_q_heads, num_kv_heads, head_dim,
+                    device, ElemType::kE2m1);
 }
 
 int pkv_num_splits(int num_seqs, int max_query_len, int max_seq_len, int num_q_heads,
@@ -574,6 +663,46 @@ pkv_status pkv_attention_varlen_e4m3(const void* q, const void* k_cache, const v
                    num_q_heads, num_kv_heads, head_dim, block_size, softmax_scale, k_scale,
                    v_scale, causal, 0, num_splits, workspace, workspace_bytes, error_flag,
                    num_blocks, ElemType::kE4m3, stream);
+}
+
+pkv_status pkv_attention_varlen_e2m1(const void* q, const void* k_cache, const void* v_cache,
+                                     void* out, float* lse_out, const int32_t* query_start_loc,
+                                     const int32_t* seq_lens, const int32_t* block_table,
+                                     int max_blocks_per_seq, int num_seqs, int64_t num_tokens,
+                                     int max_query_len, int max_seq_len, int num_q_heads,
+                                     int num_kv_heads, int head_dim, int block_size,
+                                     float softmax_scale, float k_scale, float v_scale, int causal,
+                                     int window, int num_splits, void* workspace,
+                                     size_t workspace_bytes, int32_t* error_flag,
+                                     int64_t num_blocks, void* stream) {
+  if (!valid_scale(k_scale) || !valid_scale(v_scale) || window < 0) return PKV_ERR_INVALID_ARG;
+  return attention(q, k_cache, v_cache, out, lse_out, query_start_loc, seq_lens, block_table,
+                   max_blocks_per_seq, num_seqs, num_tokens, max_query_len, max_seq_len,
+                   num_q_heads, num_kv_heads, head_dim, block_size, softmax_scale, k_scale,
+                   v_scale, causal, window, num_splits, workspace, workspace_bytes, error_flag,
+                   num_blocks, ElemType::kE2m1, stream);
+}
+
+pkv_status pkv_write_attention_varlen_e2m1(
+    const void* k_new, const void* v_new, const int64_t* slot_mapping, const void* q,
+    void* k_cache, void* v_cache, void* out, float* lse_out, const int32_t* query_start_loc,
+    const int32_t* seq_lens, const int32_t* block_table, int max_blocks_per_seq, int num_seqs,
+    int64_t num_tokens, int max_query_len, int max_seq_len, int num_q_heads, int num_kv_heads,
+    int head_dim, int block_size, float softmax_scale, float k_scale, float v_scale, int causal,
+    int window, int num_splits, void* workspace, size_t workspace_bytes, int32_t* error_flag,
+    int64_t num_blocks, void* stream) {
+  if (!valid_scale(k_scale) || !valid_scale(v_scale) || window < 0) return PKV_ERR_INVALID_ARG;
+  // the attention's own checks come first, so a refused call writes nothing
+  if (num_tokens > 0 && num_seqs > 0) {
+    if (!k_new || !v_new || !slot_mapping) return PKV_ERR_INVALID_ARG;
+    if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(slot_mapping, 8))
+      return PKV_ERR_INVALID_ARG;
+  }
+  return attention(q, k_cache, v_cache, out, lse_out, query_start_loc, seq_lens, block_table,
+                   max_blocks_per_seq, num_seqs, num_tokens, max_query_len, max_seq_len,
+                   num_q_heads, num_kv_heads, head_dim, block_size, softmax_scale, k_scale,
+                   v_scale, causal, window, num_splits, workspace, workspace_bytes, error_flag,
+                   num_blocks, ElemType::kE2m1, stream, k_new, v_new, slot_mapping);
 }
 
 int pkv_cascade_splits(int64_t num_tokens, int shared_blocks, int num_q_heads, int num_kv_heads,

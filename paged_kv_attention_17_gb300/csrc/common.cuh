@@ -6,6 +6,7 @@
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "pkv.h"
@@ -18,7 +19,7 @@ struct e4m3_t {
 };
 
 // Cache element type of a launch.
-enum class ElemType { kF32, kBf16, kE4m3 };
+enum class ElemType { kF32, kBf16, kE4m3, kE2m1 };
 
 constexpr int kBlock = 16;                       // tokens per KV-cache block
 constexpr int kDecodeMaxQ = PKV_DECODE_MAX_QLEN; // decode-class bound on q_len

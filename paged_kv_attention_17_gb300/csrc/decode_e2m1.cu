@@ -1,0 +1,626 @@
+// Attention over a 4-bit E2M1 cache: decode rows, and long requests in 16-row
+// tiles where the tensor-core prefill does not apply.
+//
+// "Inside the engine: kernels, CUDA graphs and the life of a request":
+// "Never materialise the TxT matrix" (online softmax), "Prefill has a full
+// grid; decode at batch 1 has almost none" (split-KV partials, merged by the
+// combine kernel) and "Attention over a block table, not a contiguous tensor".
+//
+// Mathematics.  With k = t_k s_k c_k and v = t_v s_v c_v (t a tensor's scale, s a
+// block's E4M3 scale, c an E2M1 code), the products s c are f16 values, so both
+// contractions run on mma.sync m16n8k16 with f16 operands over exactly what the
+// cache holds; t_k joins the score scale and t_v the final 1 / l.  q rows enter
+// as f16 scaled by a power of two per row (the row's largest magnitude in
+// [2^14, 2^15); exact for every element within 2^31 of it).  p = 2^(x - m) is
+// rounded to f16 for P V: the output divides by the sum of the rounded p (taken
+// by one more MMA against ones), so it is an exact weighted average of V rows;
+// the log-sum-exp uses the fp32 sum of p.
+//
+// Layout.  One CTA = (split, KV head, tile of 8 or 16 rows of one request); a
+// row is (new token, query head of the group).  Both contractions are taken
+// transposed (S^T = K Q^T, O^T = V^T P^T), so keys and output dims fill the MMA's
+// 16 rows and the tile's rows its 8 columns.  Every warp streams its own pairs
+// of 16-token blocks (32 keys) through its own ring of cp.async stages: no
+// barrier between warps until the merge.
+//   K: lane (g, q) holds key rows kappa(g) and kappa(g) + 8, and of each the
+//   D / 4 consecutive elements at q D / 4: one 16-byte load of codes whose
+//   bytes are MMA operand pairs in order, and its own two block scales.
+//   V: lane (g, q) holds the D / 8 elements at g D / 8 (one block scale) of keys
+//   q, (q ^ 1) + 4 and the same + 8, nibbles interleaved so a byte is the two
+//   keys of an operand pair.
+//   kappa(2 q) = q, kappa(2 q + 1) = (q ^ 1) + 4 makes the transposed score
+//   fragment (movmatrix) the P^T operand of those V keys, keeps K's row loads
+//   free of bank conflicts, and V's at two ways.
+#include <cmath>
+
+#include "e2m1.cuh"
+
+namespace pkv {
+
+namespace {
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// D += A B: 16x16 f16 A (rows g, g + 8; k 2q, 2q + 1 and + 8), 16x8 f16 B (column
+// g), fp32 D (rows g: d0, d1; g + 8: d2, d3; columns 2q, 2q + 1)
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// 16 bytes to shared memory; bytes = 0 writes zeros and reads nothing
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+template <int WORDS>
+__device__ __forceinline__ void lds_words(uint32_t (&w)[WORDS], uint32_t addr) {
+  if constexpr (WORDS == 4) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(addr)
+                 : "memory");
+  } else if constexpr (WORDS == 2) {
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                 : "=r"(w[0]), "=r"(w[1])
+                 : "r"(addr)
+                 : "memory");
+  } else {
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
+  }
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// p = 2^(x - ref) is kept below 2^(kSlack + kLift): the reference of a row moves
+// only when a score passes it by more than kSlack + kLift, and it is set
+// kLift below the row's maximum, so a row's largest p is at least 2^kLift and
+// f16's subnormals (below 2^-14) start 2^21 under it.
+constexpr float kSlack = 7.f, kLift = 7.f;
+
+template <int D, int NT>
+struct Cfg {
+  using P = E2m1Page<D>;
+  static constexpr int kWarps = 8;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kPair = 2;                        // blocks per stage
+  static constexpr int kPairKeys = kPair * kBlock;
+  // stage: K codes of both blocks, V codes, K scales, V scales
+  static constexpr int kStageBytes = 2 * kPair * P::kBytes;
+  static constexpr int kScaleOff = 2 * kPair * P::kCodes;
+  static constexpr int kStages = 3;
+  static constexpr int kRing = kWarps * kStages * kStageBytes;
+  static constexpr int kMerge = kWarps * kRows * (D + 3) * 4;
+  static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
+  static constexpr int kCtas = NT == 1 ? 2 : 1;          // per SM
+};
+
+}  // namespace
+
+template <int D, int NT>
+__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, (Cfg<D, NT>::kCtas))
+    decode_e2m1_kernel(const AttnArgs a) {
+  using C = Cfg<D, NT>;
+  using P = E2m1Page<D>;
+  constexpr int kKWords = D / 32;                        // code words of a lane's K row part
+  constexpr int kVWords = D / 64;                        // code words of a lane's V row part
+  constexpr int kMT = D / 16;                            // 16-dim tiles of O^T, MMAs of a key block
+  constexpr int R = C::kRows;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g8 = lane >> 2, t4 = lane & 3;
+
+  // released only after the wait: a prefill behind this grid may count on
+  // every input being complete
+  pdl_wait_primary();
+  pdl_launch_dependents();
+
+  const int kvh = static_cast<int>(blockIdx.x) % a.hkv;
+  const int split = static_cast<int>(blockIdx.x) / a.hkv;
+  const int r = blockIdx.z;
+  const int q0 = __ldg(a.qsl + r), q1 = __ldg(a.qsl + r + 1), L = __ldg(a.seq_lens + r);
+  const int n = q1 - q0;
+  if (n == 0) return;
+  if (n < 0 || q0 < 0 || q1 > a.num_tokens || n > L || n > a.max_query_len ||
+      (L + kBlock - 1) / kBlock > a.max_blocks_per_seq) {
+    if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0)
+      raise_flag(a.flag, PKV_FLAG_BAD_LENGTHS);
+    return;
+  }
+  const bool decode_class = n <= kDecodeMaxQ;
+  if (!decode_class && (!a.long_rows || split > 0)) return;   // (long requests are not split)
+  const int splits = decode_class ? a.num_splits : 1;
+  const int group = a.group;
+  const int rows_total = group * n;
+  const int rho0 = blockIdx.y * R;
+  if (rho0 >= rows_total) return;
+  const int nrows = min(R, rows_total - rho0);
+  const int i_first = rho0 / group, i_last = (rho0 + nrows - 1) / group;
+  // the tile's key range, and this split's run of its blocks
+  const int kv_hi = a.causal ? L - n + i_last + 1 : L;
+  const int kv_lo = a.window > 0 ? max(0, L - n + i_first - a.window + 1) : 0;
+  const int blk_lo = kv_lo / kBlock;
+  const int nb = (kv_hi + kBlock - 1) / kBlock - blk_lo;
+  const int per = (nb + splits - 1) / splits;
+  const int b_beg = blk_lo + min(nb, split * per), b_end = blk_lo + min(nb, (split + 1) * per);
+  const int npairs = (b_end - b_beg + C::kPair - 1) / C::kPair;
+  // keys every row of the tile sees: [in_lo, in_hi)
+  const int in_hi = min(a.causal ? L - n + i_first + 1 : L, b_end * kBlock);
+  const int in_lo = a.window > 0 ? max(0, L - n + i_last - a.window + 1) : 0;
+  const int cap = min(kv_hi, b_end * kBlock);            // keys the split may see
+
+  // ---- this lane's q rows as f16 fragments, and its score columns' scales ----
+  uint32_t qf[NT][kMT][2];
+  float sc[NT][2];
+  int lim[NT][2], low[NT][2];                            // visible keys of columns 2 t4, + 1
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int rr = rho0 + 8 * nt + g8;
+    uint32_t w[kMT * 2];
+#pragma unroll
+    for (int c = 0; c < kMT * 2; ++c) w[c] = 0;
+    if (rr < rows_total) {
+      const uint4* src = reinterpret_cast<const uint4*>(
+          static_cast<const __nv_bfloat16*>(a.q) +
+          (static_cast<int64_t>(q0 + rr / group) * a.hq + kvh * group + rr % group) * D +
+          t4 * (D / 4));
+#pragma unroll
+      for (int c = 0; c < kMT / 2; ++c) {
+        const uint4 v = __ldg(src + c);
+        w[4 * c] = v.x;
+        w[4 * c + 1] = v.y;
+        w[4 * c + 2] = v.z;
+        w[4 * c + 3] = v.w;
+      }
+    }
+    uint32_t mx = 0;
+#pragma unroll
+    for (int c = 0; c < kMT * 2; ++c) mx = __vmaxu2(mx, w[c] & 0x7FFF7FFFu);
+    mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    const uint32_t m16 = max(mx & 0xFFFFu, mx >> 16);
+    // largest |q| in [2^E, 2^(E+1)): e = E - 14 (clamped so 2^-e and 2^e are
+    // normal floats; a zero row takes the lower bound)
+    const int e = min(max(static_cast<int>(m16 >> 7) - 127 - 14, -100), 113);
+    const float down = __int_as_float((127 - e) << 23);
+#pragma unroll
+    for (int c = 0; c < kMT * 2; ++c)
+      qf[nt][c >> 1][c & 1] = pack_f16x2(bf16_lo(w[c]) * down, bf16_hi(w[c]) * down);
+    const float row_sc = a.scale_log2 * __int_as_float((127 + e) << 23);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      sc[nt][c] = __shfl_sync(0xffffffffu, row_sc, (2 * t4 + c) * 4);
+      const int i = min(rho0 + 8 * nt + 2 * t4 + c, rows_total - 1) / group;
+      lim[nt][c] = min(a.causal ? L - n + i + 1 : L, cap);
+      low[nt][c] = a.window > 0 ? L - n + i - a.window + 1 : 0;
+    }
+  }
+
+  // ---- the warp's ring: pair u = warp + k * kWarps, k = 0, 1, ... ----
+  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) +
+                        warp * (C::kStages * C::kStageBytes);
+  const int32_t* table = a.block_table + static_cast<int64_t>(r) * a.max_blocks_per_seq;
+  const int npw = npairs > warp ? (npairs - warp - 1) / C::kWarps + 1 : 0;
+  const uint8_t* kbase = static_cast<const uint8_t*>(a.k_cache) + static_cast<int64_t>(kvh) * P::kBytes;
+  const uint8_t* vbase = static_cast<const uint8_t*>(a.v_cache) + static_cast<int64_t>(kvh) * P::kBytes;
+  const int64_t page_stride = static_cast<int64_t>(a.hkv) * P::kBytes;
+  // table entries of 16 consecutive pairs of the warp, two a lane pair
+  auto load_ids = [&](int k0) -> int32_t {
+    const int k = k0 + (lane >> 1);
+    const int blk = b_beg + C::kPair * (warp + k * C::kWarps) + (lane & 1);
+    if (k >= npw || blk >= b_end) return -1;
+    const int32_t id = __ldg(table + blk);
+    if (id < 0 || id >= a.num_blocks) {
+      raise_flag(a.flag, PKV_FLAG_BAD_BLOCK);
+      return -1;
+    }
+    return id;
+  };
+  int32_t ids = load_ids(0);
+  auto issue = [&](int k) {
+    if (k < npw) {
+      if ((k & 15) == 0 && k > 0) ids = load_ids(k);
+      const uint32_t st = ring + (k % C::kStages) * C::kStageBytes;
+#pragma unroll
+      for (int p = 0; p < 2 * C::kPair; ++p) {           // K of both blocks, V of both
+        const int32_t id = __shfl_sync(0xffffffffu, ids, 2 * (k & 15) + (p & 1));
+        const uint8_t* page = (p < C::kPair ? kbase : vbase) + max(id, 0) * page_stride;
+        const uint32_t bytes = id >= 0 ? 16 : 0;         // (a missing block: zeros)
+#pragma unroll
+        for (int c = 0; c < P::kCodes / 512; ++c)
+          cp_async16(st + p * P::kCodes + c * 512 + lane * 16, page + c * 512 + lane * 16, bytes);
+      }
+      // the four scale areas, kScales / 16 chunks each
+      constexpr int kSC = P::kScales / 16;
+      const int p = lane / kSC, c = lane % kSC;
+      const int32_t id = __shfl_sync(0xffffffffu, ids, 2 * (k & 15) + (p & 1));
+      if (p < 2 * C::kPair) {
+        const uint8_t* page = (p < C::kPair ? kbase : vbase) + max(id, 0) * page_stride;
+        cp_async16(st + C::kScaleOff + p * P::kScales + c * 16, page + P::kCodes + c * 16,
+                   id >= 0 ? 16 : 0);
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int k = 0; k < C::kStages - 1; ++k) issue(k);
+
+  const int ka = (g8 & 1) ? ((g8 >> 1) ^ 1) + 4 : g8 >> 1;   // kappa(g8); the lane's other key + 8
+  const int kv[4] = {t4, (t4 ^ 1) + 4, t4 + 8, (t4 ^ 1) + 12};
+  float oacc[NT][kMT][4];
+  float ref[NT][2], l[NT][2], lr[NT][4];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int i = 0; i < kMT; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) oacc[nt][i][c] = 0.f;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      ref[nt][c] = -INFINITY;
+      l[nt][c] = 0.f;
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) lr[nt][c] = 0.f;
+  }
+
+  for (int k = 0; k < npw; ++k) {
+    cp_async_wait<C::kStages - 2>();
+    __syncwarp();                                        // every lane's part of stage k has landed
+    issue(k + C::kStages - 1);                           // (into the stage read in step k - 1)
+    const uint32_t st = ring + (k % C::kStages) * C::kStageBytes;
+    const int key0 = (b_beg + C::kPair * (warp + k * C::kWarps)) * kBlock;
+    const bool edge = key0 + C::kPairKeys > in_hi || key0 < in_lo;
+
+    // S^T of both blocks
+    float s[C::kPair][NT][4];
+#pragma unroll
+    for (int j = 0; j < C::kPair; ++j) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[j][nt][c] = 0.f;
+      uint32_t wa[kKWords], wb[kKWords], sa[2], sb[2];
+      const uint32_t row = st + j * P::kCodes + ka * P::kRowCodes + t4 * (D / 8);
+      lds_words<kKWords>(wa, row);
+      lds_words<kKWords>(wb, row + 8 * P::kRowCodes);
+      const uint32_t srow = st + C::kScaleOff + j * P::kScales + ka * P::kRowScales + t4 * (D / 64);
+      if constexpr (D == 128) {
+        const uint32_t ha = scales2_to_f16x2(lds_u16(srow));
+        const uint32_t hb = scales2_to_f16x2(lds_u16(srow + 8 * P::kRowScales));
+        sa[0] = byte_perm(ha, ha, 0x1010);
+        sa[1] = byte_perm(ha, ha, 0x3232);
+        sb[0] = byte_perm(hb, hb, 0x1010);
+        sb[1] = byte_perm(hb, hb, 0x3232);
+      } else {
+        const uint32_t ca = lds_u8(srow), cb = lds_u8(srow + 8 * P::kRowScales);
+        sa[0] = sa[1] = scales2_to_f16x2(ca * 0x0101u);
+        sb[0] = sb[1] = scales2_to_f16x2(cb * 0x0101u);
+      }
+#pragma unroll
+      for (int w = 0; w < kKWords; ++w) {
+        uint32_t ra[4], rb[4];
+        e2m1x8_to_f16x2x4(wa[w], ra);
+        e2m1x8_to_f16x2x4(wb[w], rb);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          ra[c] = mul_f16x2(ra[c], sa[w >> 1]);
+          rb[c] = mul_f16x2(rb[c], sb[w >> 1]);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_f16(s[j][nt], ra[0], rb[0], ra[1], rb[1], qf[nt][2 * w][0], qf[nt][2 * w][1]);
+          mma_f16(s[j][nt], ra[2], rb[2], ra[3], rb[3], qf[nt][2 * w + 1][0],
+                  qf[nt][2 * w + 1][1]);
+        }
+      }
+    }
+    // scale (log2 domain) and mask
+#pragma unroll
+    for (int j = 0; j < C::kPair; ++j)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          s[j][nt][c] *= sc[nt][c & 1];
+          if (edge) {
+            const int key = key0 + j * kBlock + ka + (c >> 1) * 8;
+            if (key >= lim[nt][c & 1] || key < low[nt][c & 1]) s[j][nt][c] = -INFINITY;
+          }
+        }
+    // move a row's reference when a score passes it by kSlack + kLift
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float mx[2];
+      bool up = false;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        mx[c] = fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2]));
+        up = up || mx[c] > ref[nt][c] + (kSlack + kLift);
+      }
+      if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1)
+            mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], o));
+          if (mx[c] > ref[nt][c] + (kSlack + kLift)) {
+            const float to = mx[c] - kLift;
+            const float f = ex2(ref[nt][c] - to);        // (0 from the start's -inf)
+            ref[nt][c] = to;
+            l[nt][c] *= f;
+            lr[nt][c] *= f;
+            lr[nt][c + 2] *= f;
+#pragma unroll
+            for (int i = 0; i < kMT; ++i) {
+              oacc[nt][i][c] *= f;
+              oacc[nt][i][c + 2] *= f;
+            }
+          }
+        }
+      }
+    }
+    // p, its sums, and P^T operands
+    uint32_t pf[C::kPair][NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float base[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) base[c] = ref[nt][c] == -INFINITY ? 0.f : ref[nt][c];
+#pragma unroll
+      for (int j = 0; j < C::kPair; ++j) {
+        float p[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          p[c] = ex2(s[j][nt][c] - base[c & 1]);
+          l[nt][c & 1] += p[c];
+        }
+        pf[j][nt][0] = movmatrix_t(pack_f16x2(p[0], p[1]));
+        pf[j][nt][1] = movmatrix_t(pack_f16x2(p[2], p[3]));
+        // the sums of the rounded p: against a V of ones
+        mma_f16(lr[nt], 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, pf[j][nt][0],
+                pf[j][nt][1]);
+      }
+    }
+    // O^T += V^T P^T
+#pragma unroll
+    for (int j = 0; j < C::kPair; ++j) {
+      const uint32_t vrow = st + (C::kPair + j) * P::kCodes + g8 * (D / 16);
+      const uint32_t srow = st + C::kScaleOff + (C::kPair + j) * P::kScales + g8 * D / 128;
+      uint32_t vw[4][kVWords], cs[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        lds_words<kVWords>(vw[c], vrow + kv[c] * P::kRowCodes);
+        cs[c] = lds_u8(srow + kv[c] * P::kRowScales);
+      }
+      if (edge) {
+        // p is 0 outside a row's keys, and so must p v be whatever a hidden slot
+        // holds: a scale outside the tile's keys, or a NaN one that some row of
+        // the tile may not see, counts as 0 (a 0 code times any finite scale)
+        bool bad = false;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int key = key0 + j * kBlock + kv[c];
+          const bool nan = (cs[c] & 0x7F) == 0x7F;
+          const bool in = key < cap && key >= kv_lo;
+          bad = bad || (nan && in);
+          if (nan || !in) cs[c] = 0;
+          if (nan && in) cs[c] = 0x100;                  // remembered below
+        }
+        if (__any_sync(0xffffffffu, bad)) {
+          // rows that do see such a key take the NaN in its block's dims
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t v = __shfl_sync(0xffffffffu, cs[c], g8 * 4 + q);
+              const int key = key0 + j * kBlock + ((c & 1) ? (q ^ 1) + 4 : q) + (c >> 1) * 8;
+              if (v == 0x100) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e)
+                    if (key < lim[nt][e] && key >= low[nt][e]) {
+#pragma unroll
+                      for (int i = 0; i < kMT; ++i)
+                        oacc[nt][i][e] = oacc[nt][i][e + 2] = __int_as_float(0x7FC00000);
+                    }
+              }
+            }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) cs[c] &= 0xFF;
+        }
+      }
+      const uint32_t s01 = scales2_to_f16x2(cs[0] | (cs[1] << 8));
+      const uint32_t s23 = scales2_to_f16x2(cs[2] | (cs[3] << 8));
+#pragma unroll
+      for (int w = 0; w < kVWords; ++w) {
+        // byte i of e: element 2 i of both keys of a pair; of o: element 2 i + 1
+        constexpr uint32_t kLow = 0x0F0F0F0Fu;
+        uint32_t e01[4], o01[4], e23[4], o23[4];
+        e2m1x8_to_f16x2x4((vw[0][w] & kLow) | ((vw[1][w] << 4) & ~kLow), e01);
+        e2m1x8_to_f16x2x4(((vw[0][w] >> 4) & kLow) | (vw[1][w] & ~kLow), o01);
+        e2m1x8_to_f16x2x4((vw[2][w] & kLow) | ((vw[3][w] << 4) & ~kLow), e23);
+        e2m1x8_to_f16x2x4(((vw[2][w] >> 4) & kLow) | (vw[3][w] & ~kLow), o23);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t a0 = mul_f16x2(e01[i], s01), a1 = mul_f16x2(o01[i], s01);
+          const uint32_t a2 = mul_f16x2(e23[i], s23), a3 = mul_f16x2(o23[i], s23);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma_f16(oacc[nt][4 * w + i], a0, a1, a2, a3, pf[j][nt][0], pf[j][nt][1]);
+        }
+      }
+    }
+    __syncwarp();                                        // the stage is read; step k + 1 refills it
+  }
+  cp_async_wait<0>();
+  __syncthreads();                                       // every ring is idle: reuse for the merge
+
+  // ---- merge of the warps' (ref, l, acc) ----
+  float* mw = reinterpret_cast<float*>(smem);            // [warp][row]
+  float* lw = mw + C::kWarps * R;
+  float* lrw = lw + C::kWarps * R;
+  float* aw = lrw + C::kWarps * R;                       // [warp][row][D]
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float lt = l[nt][c];
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
+      const int rho = 8 * nt + 2 * t4 + c;
+      if (g8 == 0) {
+        mw[warp * R + rho] = ref[nt][c];
+        lw[warp * R + rho] = lt;
+        lrw[warp * R + rho] = lr[nt][c];
+      }
+#pragma unroll
+      for (int i = 0; i < kMT; ++i)
+        *reinterpret_cast<float2*>(aw + (warp * R + rho) * D + g8 * (D / 8) + 2 * i) =
+            make_float2(oacc[nt][i][c], oacc[nt][i][c + 2]);
+    }
+  __syncthreads();
+  constexpr int kDPL = D / 32;
+  for (int rho = warp; rho < nrows; rho += C::kWarps) {
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < C::kWarps; ++w) M = fmaxf(M, mw[w * R + rho]);
+    float o[kDPL];
+#pragma unroll
+    for (int e = 0; e < kDPL; ++e) o[e] = 0.f;
+    float lsum = 0.f, lnorm = 0.f;
+#pragma unroll
+    for (int w = 0; w < C::kWarps; ++w) {
+      // (a row whose scores are all NaN keeps -inf in every warp: weight 1)
+      const float m = mw[w * R + rho];
+      const float f = m == M ? 1.f : ex2(m - M);
+      lsum = fmaf(f, lw[w * R + rho], lsum);
+      lnorm = fmaf(f, lrw[w * R + rho], lnorm);
+      const float* src = aw + (w * R + rho) * D + lane * kDPL;
+#pragma unroll
+      for (int e = 0; e < kDPL; ++e) o[e] = fmaf(f, src[e], o[e]);
+    }
+    // (a NaN sum stays a NaN: only a row without a key takes 0)
+    const float inv = lnorm == 0.f ? 0.f : a.v_scale / lnorm;
+    const float lse2 = lsum == 0.f ? -INFINITY : M + lg2(lsum);
+    const int rr = rho0 + rho, i = rr / group, h = kvh * group + rr % group;
+    if (splits > 1) {
+      const int64_t w =
+          ((static_cast<int64_t>(split) * a.num_seqs + r) * kDecodeMaxQ + i) * a.hq + h;
+      float* dst = a.ws_o + w * D + lane * kDPL;
+      if constexpr (kDPL == 4)
+        *reinterpret_cast<float4*>(dst) =
+            make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+      else
+        *reinterpret_cast<float2*>(dst) = make_float2(o[0] * inv, o[1] * inv);
+      if (lane == 0) a.ws_lse[w] = lse2;
+    } else {
+      const int64_t t = q0 + i;
+      __nv_bfloat16* dst =
+          static_cast<__nv_bfloat16*>(a.out) + (t * a.hq + h) * D + lane * kDPL;
+      if constexpr (kDPL == 4)
+        *reinterpret_cast<uint2*>(dst) =
+            make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+      else
+        *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(o[0] * inv, o[1] * inv);
+      if (a.lse_out != nullptr && lane == 0) a.lse_out[t * a.hq + h] = lse2 * kLn2;
+    }
+  }
+}
+
+template <int D, int NT>
+static cudaError_t launch_t(const AttnArgs& a, int row_tiles, cudaStream_t stream) {
+  using C = Cfg<D, NT>;
+  static unsigned done = 0;                              // one bit per device already configured
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 32 || !((done >> dev) & 1u)) {
+    e = cudaFuncSetAttribute(decode_e2m1_kernel<D, NT>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(decode_e2m1_kernel<D, NT>,
+                               cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    if (e != cudaSuccess) return e;
+    if (dev < 32) done |= 1u << dev;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.hkv * a.num_splits),
+                     static_cast<unsigned>(row_tiles), static_cast<unsigned>(a.num_seqs));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode_e2m1_kernel<D, NT>, a);
+}
+
+// Rows per tile: 8 where no request's rows exceed them, else 16 (a tile's
+// cached rows are read once for all of its rows).
+int decode_e2m1_rows_per_tile(int group, int max_query_len, bool long_rows) {
+  const int64_t q = long_rows ? max_query_len : (max_query_len < kDecodeMaxQ ? max_query_len : kDecodeMaxQ);
+  return group * (q < 1 ? 1 : q) <= 8 ? 8 : 16;
+}
+
+// Resident CTAs per SM for that tile height.
+int decode_e2m1_ctas_per_sm(int rows_per_tile) {
+  return rows_per_tile == 8 ? Cfg<128, 1>::kCtas : Cfg<128, 2>::kCtas;
+}
+
+cudaError_t launch_decode_e2m1(const AttnArgs& a, int head_dim, cudaStream_t stream) {
+  const int R = decode_e2m1_rows_per_tile(a.group, a.max_query_len, a.long_rows != 0);
+  const int64_t q = a.long_rows || a.max_query_len < kDecodeMaxQ ? a.max_query_len : kDecodeMaxQ;
+  const int64_t row_tiles = (a.group * q + R - 1) / R;
+  if (row_tiles < 1 || row_tiles > 65535 || a.num_seqs > 65535)
+    return cudaErrorInvalidConfiguration;
+  const int tiles = static_cast<int>(row_tiles);
+  if (head_dim == 128)
+    return R == 8 ? launch_t<128, 1>(a, tiles, stream) : launch_t<128, 2>(a, tiles, stream);
+  return R == 8 ? launch_t<64, 1>(a, tiles, stream) : launch_t<64, 2>(a, tiles, stream);
+}
+
+}  // namespace pkv
