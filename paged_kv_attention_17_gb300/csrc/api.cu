@@ -356,10 +356,12 @@ static pkv_status attention(const void* q, const void* k_cache, const void* v_ca
   }
   if (e == cudaSuccess && splits > 1) e = launch_combine(a, et, head_dim, st);
   if (e == cudaSuccess && tc_prefill && max_query_len > kDecodeMaxQ) {
-    CUtensorMap qmap, kmap_sw, vmap_sw;
+    // (E2M1 pages come by untiled bulk copies: no maps)
+    CUtensorMap qmap, kmap_sw = {}, vmap_sw = {};
     if (num_tokens > 0x7FFFFFFFll || !encode_q_map(&qmap, q, num_tokens, num_q_heads, head_dim) ||
-        !encode_cache_map(&kmap_sw, k_cache, num_slots, num_kv_heads, head_dim, et, true) ||
-        !encode_cache_map(&vmap_sw, v_cache, num_slots, num_kv_heads, head_dim, et, true))
+        (et != ElemType::kE2m1 &&
+         (!encode_cache_map(&kmap_sw, k_cache, num_slots, num_kv_heads, head_dim, et, true) ||
+          !encode_cache_map(&vmap_sw, v_cache, num_slots, num_kv_heads, head_dim, et, true))))
       return PKV_ERR_CUDA;
     // the decode kernel (and the combine) ahead of it release it only after
     // their own dependency waits: its inputs are complete at launch

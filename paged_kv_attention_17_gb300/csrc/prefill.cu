@@ -47,9 +47,19 @@
 // element within 2^31 of the largest), and scales its scores back by 2^e
 // together with softmax_scale * k_scale; P goes to TMEM as f16 and v_scale
 // joins the final 1 / l.
+//
+// E2M1 caches (head_dim 64 and 128): the same, with a tile's pages (8 blocks of
+// 16 rows of codes and block scales, 9216 or 4608 bytes) brought by one untiled
+// bulk copy each into the end of the ring slot, and widened to the f16 products
+// scale * code, which f16 holds exactly.  P is lifted by 2^7 (the reference set
+// 7 below the row's maximum), so that f16's subnormals start 2^21 under a row's
+// largest p.  A NaN scale of V in a tile that crosses a mask edge is widened to
+// zeros and noted: the rows that see its key take the NaN at the end, the rows
+// that do not are untouched (0 * NaN would reach them through the MMA).
 #include <algorithm>
 
 #include "common.cuh"
+#include "e2m1.cuh"
 
 namespace pkv {
 
@@ -75,8 +85,18 @@ __host__ __device__ constexpr int off_bar(bool) { return kOffKV + kStages * kSta
 // code_full[K, V][stage] and q_ready
 __host__ __device__ constexpr int num_bars(bool f8) { return 1 + 4 * kStages + 6 + (f8 ? 5 : 0); }
 __host__ __device__ constexpr int off_misc(bool f8) { return off_bar(f8) + num_bars(f8) * 8; }
-__host__ __device__ constexpr int smem_alloc(bool f8) { return off_misc(f8) + 32 + 1024; }
-static_assert(smem_alloc(true) <= 232448, "E4M3 prefill shared memory");
+// E2M1: notes of NaN V scales in edge tiles, [edge tile][block of a row][key / 32],
+// after one word that says whether there is any
+constexpr int kEdgeTiles = 6;                             // 3 at each end of a key range
+constexpr int kNoteWords = 1 + kEdgeTiles * 8 * (kKeys / 32);
+__host__ __device__ constexpr int off_notes() { return off_misc(true) + 32; }
+__host__ __device__ constexpr int smem_alloc(bool f8) {
+  return off_misc(f8) + 32 + (f8 ? kNoteWords * 4 : 0) + 1024;
+}
+static_assert(smem_alloc(true) <= 232448, "code prefill shared memory");
+// cache types of the kernel
+constexpr int kKvBf16 = 0, kKvE4m3 = 1, kKvE2m1 = 2;
+constexpr float kE2m1Lift = 7.f;
 // TMEM: S_t in columns [128 t, 128 t + 128) - its first 64 columns take P_t
 // (bf16 pairs) once the scores are read - and O_t in [256 + 128 t, ...).
 constexpr int kTmemCols = 512;
@@ -270,6 +290,25 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
                "r"(v.z), "r"(v.w)
                : "memory");
 }
+// contiguous bytes (16-byte aligned, a multiple of 16) to shared memory
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar,
+                                          uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1], %2, [%3], %4;" ::"r"(smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
 // bf16 pair -> fp32 pair scaled by f (exact: a power of two in range)
 __device__ __forceinline__ uint32_t bf16x2_to_f16x2_scaled(uint32_t w, float f) {
   return pack_f16(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
@@ -279,14 +318,19 @@ __device__ __forceinline__ uint32_t bf16x2_to_f16x2_scaled(uint32_t w, float f) 
 
 // D: head_dim, 128 or 64.  The layouts are those of D = 128 (two 64-column
 // halves of Q, K and V, O_t in 128 TMEM columns); D = 64 fills one half of
-// each and the first 64 columns of O_t.  F8: an E4M3 cache (D = 128).
-template <int D, bool F8>
-__global__ void __launch_bounds__(threads_for(F8), 1)
+// each and the first 64 columns of O_t.  KV: the cache's type (E4M3: D = 128).
+template <int D, int KV>
+__global__ void __launch_bounds__(threads_for(KV != kKvBf16), 1)
     prefill_kernel(const __grid_constant__ CUtensorMap qmap,
                    const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap, const AttnArgs a) {
   static_assert(D == 64 || D == 128, "head_dim 64 or 128");
-  static_assert(!F8 || D == 128, "E4M3 tiles at head_dim 128");
+  static_assert(KV != kKvE4m3 || D == 128, "E4M3 tiles at head_dim 128");
+  constexpr bool F8 = KV != kKvBf16;                     // codes, widened by warps 10 and 11
+  constexpr bool E2 = KV == kKvE2m1;
+  using Page = E2m1Page<D>;
+  // a tile's pages end its ring slot: 2 kHalf bytes for K, as many for V
+  constexpr int kPagesOff = 2 * kHalf - (kKeys / kBlock) * Page::kBytes;
   constexpr int kThreads = threads_for(F8);
   constexpr int kH = D / 64;                             // 64-column halves of a row
   constexpr int kOC = D / 32;                            // 32-column chunks of an O row
@@ -309,6 +353,7 @@ __global__ void __launch_bounds__(threads_for(F8), 1)
   uint64_t* code_full = bars + num_bars(false);
   uint64_t* bar_qr = code_full + 2 * kStages;
   int* misc = reinterpret_cast<int*>(smem + off_misc(F8));   // [0] request, [1] tile, [2] tmem
+  uint32_t* notes = reinterpret_cast<uint32_t*>(smem + off_notes());   // E2M1
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool packed = a.cascade == 1;                    // shared-prefix mode
@@ -428,6 +473,19 @@ __global__ void __launch_bounds__(threads_for(F8), 1)
     }
   }
 
+  // E2M1: tile kt's place in the notes, -1 if every row of the unit sees all of
+  // its keys (each end of the unit's rows spans at most 256 keys: 3 tiles)
+  auto edge_tile = [&](int kt) {
+    const int key0 = (kt_base + kt) * kKeys;
+    const int lim_first = a.causal ? min(L - n + i0 + 1, L) : L;
+    const int lo_last = a.window > 0 ? L - n + i_hi - a.window + 1 : 0;
+    if (key0 + kKeys > lim_first && ntk - 1 - kt < kEdgeTiles / 2) return ntk - 1 - kt;
+    if (key0 < lo_last && kt < kEdgeTiles / 2) return kEdgeTiles / 2 + kt;
+    return -1;
+  };
+  if constexpr (E2)
+    for (int i = threadIdx.x; i < kNoteWords; i += kThreads) notes[i] = 0;
+
   // ---- barriers and TMEM ----
   if (threadIdx.x == 0) {
     mbar_init(bar_q, 1);
@@ -468,8 +526,10 @@ __global__ void __launch_bounds__(threads_for(F8), 1)
     const int oob = static_cast<int>(a.num_blocks * kBlock);   // a slot past the cache
     if (lane == 0) {
       tma_prefetch_desc(&qmap);
-      tma_prefetch_desc(&kmap);
-      tma_prefetch_desc(&vmap);
+      if constexpr (!E2) {
+        tma_prefetch_desc(&kmap);
+        tma_prefetch_desc(&vmap);
+      }
       mbar_arrive_expect_tx(bar_q, 2 * kH * kHalf);
       const uint64_t pol_q = l2_policy_evict_first();
       for (int t = 0; t < 2; ++t)
@@ -496,6 +556,8 @@ __global__ void __launch_bounds__(threads_for(F8), 1)
       }
       const int slot = ent >= 0 ? ent * kBlock : oob;   // past the context: zero fill
       uint8_t* kst = smem + kOffKV + st * kStageBytes;
+      // E2M1: pages past the context are not loaded (their rows are zeroed)
+      const int pages = E2 ? __popc(__ballot_sync(0xffffffffu, ent >= 0)) : 0;
       // K half of the stage, then its V half, each once its previous tile is
       // done (E4M3: the codes, into the second half of the slot)
       for (int part = 0; part < 2; ++part) {
@@ -510,9 +572,16 @@ __global__ void __launch_bounds__(threads_for(F8), 1)
             break;
           }
         }
-        if (lane == 0) mbar_arrive_expect_tx(fullb, F8 ? kCodeBytes : kH * kHalf);
+        if (lane == 0)
+          mbar_arrive_expect_tx(fullb, E2 ? pages * Page::kBytes : F8 ? kCodeBytes : kH * kHalf);
         __syncwarp();
-        if (lane < kKeys / kBlock) {
+        if constexpr (E2) {
+          if (ent >= 0)
+            bulk_load(kst + part * 2 * kHalf + kPagesOff + lane * Page::kBytes,
+                      static_cast<const uint8_t*>(part == 0 ? a.k_cache : a.v_cache) +
+                          (static_cast<int64_t>(ent) * a.hkv + g) * Page::kBytes,
+                      Page::kBytes, fullb, pol_kv);
+        } else if (lane < kKeys / kBlock) {
           uint8_t* dst = kst + part * 2 * kHalf;
           const CUtensorMap* map = part == 0 ? &kmap : &vmap;
           if constexpr (F8) {
@@ -611,7 +680,87 @@ __global__ void __launch_bounds__(threads_for(F8), 1)
     }
     __syncwarp();
   } else if (warp >= 10) {
-    if constexpr (F8) {
+    if constexpr (E2) {
+      // ================= E2M1 widening (warps 10, 11) =================
+      // Unit i of thread ct: the 16 codes of one scale block of key row r, and
+      // the scale, widened into the row's two f16 chunks of that block.  Code
+      // reads of a phase are contiguous; its chunk stores hit distinct banks
+      // (at D 128 the blocks of the second column half store their chunks the
+      // other way round).  Every code of a tile is read before any f16 chunk
+      // is written, which may lie over codes.
+      constexpr int kUnits = kKeys * Page::kRowScales / 64;
+      const int ct = threadIdx.x - 10 * 32;
+      const int b = ct % Page::kRowScales, r0 = ct / Page::kRowScales;
+      constexpr int kStep = 64 / Page::kRowScales;       // rows from a unit to the next: 8 or 16
+      const int r7 = r0 & 7, c0 = 2 * (b & 3), second = b >> 2;
+      for (int kt = 0; ok && kt < ntk; ++kt) {
+        const int st = kt % kStages;
+        const int key0 = (kt_base + kt) * kKeys;
+        const int edge = edge_tile(kt);
+        for (int part = 0; part < 2; ++part) {
+          uint32_t w = 1;
+          if (lane == 0) w = mbar_wait(&code_full[part * kStages + st], (kt / kStages) & 1);
+          w = __shfl_sync(0xffffffffu, w, 0);
+          // (a wait that gave up reads whatever the slot holds; nothing of it
+          // is written before all_ok below stops both warps)
+          const uint32_t slot_base =
+              smem_u32(smem + kOffKV + st * kStageBytes + part * 2 * kHalf);
+          uint2 cw[kUnits];
+          uint32_t sw[kUnits / 4];                       // scale codes, four a word
+#pragma unroll
+          for (int i = 0; i < kUnits; ++i) {
+            const int r = r0 + i * kStep;
+            const uint32_t page = slot_base + kPagesOff + (r / kBlock) * Page::kBytes;
+            cw[i] = lds64(page + (r % kBlock) * Page::kRowCodes + b * (kQuant / 2));
+            const uint32_t sc =
+                lds8(page + Page::kCodes + (r % kBlock) * Page::kRowScales + b);
+            sw[i / 4] = i % 4 == 0 ? sc : sw[i / 4] | (sc << (8 * (i % 4)));
+          }
+          uint32_t all_ok;
+          asm volatile(
+              "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+              "bar.red.and.pred q, 1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+              : "=r"(all_ok)
+              : "r"(w)
+              : "memory");
+          if (!all_ok) {
+            ok = false;
+            break;
+          }
+          const uint32_t dst = slot_base + second * kHalf + r0 * 128;
+#pragma unroll
+          for (int i = 0; i < kUnits; ++i) {
+            const int r = r0 + i * kStep;
+            uint4 o0 = make_uint4(0, 0, 0, 0), o1 = o0;  // key rows past the context: zero
+            uint32_t sc = (sw[i / 4] >> (8 * (i % 4))) & 0xFF;
+            bool live = key0 + r < kv_len;
+            if (part == 1 && edge >= 0 && live && (sc & 0x7F) == 0x7F) {
+              atomicOr(&notes[1 + (edge * 8 + b) * (kKeys / 32) + r / 32], 1u << (r % 32));
+              atomicOr(&notes[0], 1u);
+              live = false;
+            }
+            if (live) {
+              const uint32_t s2 = scales2_to_f16x2(sc * 0x0101u);
+              uint32_t v[4];
+              e2m1x8_to_f16x2x4(cw[i].x, v);
+              o0 = make_uint4(mul_f16x2(v[0], s2), mul_f16x2(v[1], s2), mul_f16x2(v[2], s2),
+                              mul_f16x2(v[3], s2));
+              e2m1x8_to_f16x2x4(cw[i].y, v);
+              o1 = make_uint4(mul_f16x2(v[0], s2), mul_f16x2(v[1], s2), mul_f16x2(v[2], s2),
+                              mul_f16x2(v[3], s2));
+            }
+            const uint32_t row = dst + i * kStep * 128;
+            sts128(row + (((c0 + second) ^ r7) << 4), second ? o1 : o0);
+            sts128(row + (((c0 + 1 - second) ^ r7) << 4), second ? o0 : o1);
+          }
+          // the widened tile is read by the tensor cores (async proxy)
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(part == 0 ? &k_full[st] : &v_full[st]);
+        }
+      }
+      if (!ok && lane == 0) raise_flag(a.flag, PKV_FLAG_TIMEOUT);
+    } else if constexpr (F8) {
       // ================= E4M3 widening (warps 10, 11) =================
       // Unit i of thread ct: the 16 codes of 16-byte chunk j of key row
       // r = (ct % 8) + 8 i (the codes 128B-swizzled: chunk j of row r at
@@ -701,7 +850,7 @@ __global__ void __launch_bounds__(threads_for(F8), 1)
         const int sw = row & 7;
         uint32_t mx = 0;                                 // two |bf16| maxima, as integers
 #pragma unroll
-        for (int c = 0; c < 2 * 8; ++c) {
+        for (int c = 0; c < kH * 8; ++c) {
           const uint4 v = lds128(qrow + (c >> 3) * kHalf + ((c & 7) ^ sw) * 16);
           mx = __vmaxu2(mx, __vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu));
           mx = __vmaxu2(mx, __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
@@ -712,7 +861,7 @@ __global__ void __launch_bounds__(threads_for(F8), 1)
         const int e = min(max(static_cast<int>(m16 >> 7) - 127 - 14, -100), 113);
         const float down = __int_as_float((127 - e) << 23);
 #pragma unroll
-        for (int c = 0; c < 2 * 8; ++c) {
+        for (int c = 0; c < kH * 8; ++c) {
           const uint32_t pc = qrow + (c >> 3) * kHalf + ((c & 7) ^ sw) * 16;
           uint4 v = lds128(pc);
           v.x = bf16x2_to_f16x2_scaled(v.x, down);
@@ -776,7 +925,9 @@ __global__ void __launch_bounds__(threads_for(F8), 1)
       const float msafe = mnew == -INFINITY ? 0.f : mnew;
       const float alpha = ex2f_(m - msafe);
       // p = 2^(s sc - m): the scaling in packed pairs, 4 independent pair sums
-      const unsigned long long scp = pair(sc, sc), nmp = pair(-msafe, -msafe);
+      // (E2M1: lifted by 2^kE2m1Lift)
+      const float neg_ref = E2 ? kE2m1Lift - msafe : -msafe;
+      const unsigned long long scp = pair(sc, sc), nmp = pair(neg_ref, neg_ref);
       unsigned long long ps4[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
       for (int j = 0; j < kKeys / 2; ++j) {
@@ -850,6 +1001,22 @@ __global__ void __launch_bounds__(threads_for(F8), 1)
     } else {
       tc_fence_after();
       const float inv = l > 0.f ? (F8 ? a.v_scale : 1.f) / l : 0.f;
+      uint32_t nan_blocks = 0;                           // E2M1: scale blocks with a visible NaN
+      if constexpr (E2) {
+        if (notes[0] != 0) {
+          for (int e = 0; e < kEdgeTiles; ++e) {
+            const int kt = e < kEdgeTiles / 2 ? ntk - 1 - e : e - kEdgeTiles / 2;
+            const int key0 = (kt_base + kt) * kKeys;
+            for (int w = 0; w < 8 * (kKeys / 32); ++w) {
+              uint32_t m = notes[1 + e * 8 * (kKeys / 32) + w];
+              for (; m != 0; m &= m - 1) {
+                const int key = key0 + (w % (kKeys / 32)) * 32 + __ffs(m) - 1;
+                if (key < lim && key >= lo) nan_blocks |= 1u << (w / (kKeys / 32));
+              }
+            }
+          }
+        }
+      }
       if (packed) {
         // row (token, head) of the 256-row pair: fp32 partial and log2 lse
         const int64_t rho = (2 * static_cast<int64_t>(tile) + t) * kQRows + row;
@@ -878,6 +1045,11 @@ __global__ void __launch_bounds__(threads_for(F8), 1)
         float v[32];
         tmem_ld32(t_o + c * 32, v);
         if (store) {
+          if (E2 && ((nan_blocks >> (2 * c)) & 3) != 0) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if ((nan_blocks >> (2 * c + e / kQuant)) & 1) v[e] = __int_as_float(0x7FC00000);
+          }
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             uint4 w;
@@ -891,7 +1063,8 @@ __global__ void __launch_bounds__(threads_for(F8), 1)
       }
       if (store && a.lse_out != nullptr)
         a.lse_out[static_cast<int64_t>(q0 + i_r) * a.hq + h] =
-            l > 0.f ? (m + lg2f_(l)) * kLn2 : -INFINITY;
+            E2 ? (l == 0.f ? -INFINITY : (m - kE2m1Lift + lg2f_(l)) * kLn2)
+               : l > 0.f ? (m + lg2f_(l)) * kLn2 : -INFINITY;
       }
     }
     if (!ok && lane == 0) raise_flag(a.flag, PKV_FLAG_TIMEOUT);
@@ -911,7 +1084,8 @@ __global__ void __launch_bounds__(threads_for(F8), 1)
 // an odd GQA group two query tiles of one head (AttnArgs::pair_tiles).
 bool prefill_supported(int head_dim, ElemType et, int group) {
   return ((et == ElemType::kBf16 && (head_dim == 128 || head_dim == 64)) ||
-          (et == ElemType::kE4m3 && head_dim == 128)) &&
+          (et == ElemType::kE4m3 && head_dim == 128) ||
+          (et == ElemType::kE2m1 && (head_dim == 128 || head_dim == 64))) &&
          group >= 1;
 }
 
@@ -925,20 +1099,19 @@ cudaError_t launch_prefill(const AttnArgs& a, const CUtensorMap& qmap, const CUt
                            const CUtensorMap& vmap, int head_dim, ElemType et,
                            cudaStream_t stream) {
   if (!prefill_supported(head_dim, et, 1)) return cudaErrorInvalidValue;
-  const bool f8 = et == ElemType::kE4m3;
+  using Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, AttnArgs);
+  const Kernel all[] = {prefill_kernel<128, kKvBf16>, prefill_kernel<64, kKvBf16>,
+                        prefill_kernel<128, kKvE4m3>, prefill_kernel<128, kKvE2m1>,
+                        prefill_kernel<64, kKvE2m1>};
+  const bool f8 = et != ElemType::kBf16;
   static unsigned done = 0;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 32 || !((done >> dev) & 1u)) {
-    e = cudaFuncSetAttribute(prefill_kernel<128, false>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem_alloc(false));
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(prefill_kernel<64, false>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem_alloc(false));
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(prefill_kernel<128, true>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem_alloc(true));
+    for (int i = 0; i < 5 && e == cudaSuccess; ++i)
+      e = cudaFuncSetAttribute(all[i], cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               smem_alloc(i >= 2));
     if (e != cudaSuccess) return e;
     if (dev < 32) done |= 1u << dev;
   }
@@ -963,9 +1136,10 @@ cudaError_t launch_prefill(const AttnArgs& a, const CUtensorMap& qmap, const CUt
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (f8) return cudaLaunchKernelEx(&cfg, prefill_kernel<128, true>, qmap, kmap, vmap, a);
-  return head_dim == 128 ? cudaLaunchKernelEx(&cfg, prefill_kernel<128, false>, qmap, kmap, vmap, a)
-                         : cudaLaunchKernelEx(&cfg, prefill_kernel<64, false>, qmap, kmap, vmap, a);
+  const int which = et == ElemType::kBf16   ? (head_dim == 128 ? 0 : 1)
+                    : et == ElemType::kE4m3 ? 2
+                                            : (head_dim == 128 ? 3 : 4);
+  return cudaLaunchKernelEx(&cfg, all[which], qmap, kmap, vmap, a);
 }
 
 }  // namespace pkv
