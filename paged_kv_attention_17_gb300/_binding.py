@@ -441,30 +441,70 @@ def pkv_cascade_attention(q, k_cache, v_cache, out, query_start_loc, suffix_lens
 
 
 def _need(device, **tensors):
-    """Each named (tensor, dtype, shape) is a contiguous CUDA tensor of that
-    dtype and shape on the device; an entry whose tensor is None is skipped."""
+    """Raise unless each named (tensor, dtype, shape) is a contiguous tensor of
+    that dtype and shape on CUDA device ``device``; an entry whose tensor is
+    None is skipped."""
     for name, (t, dtype, shape) in tensors.items():
         if t is None:
             continue
         if t.dtype != dtype:
             raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
+        if t.get_device() != device:
+            raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
         if t.shape != shape:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
 
 
-def _e2m1_dims(k_cache):
-    """(device, num_blocks, num_kv_heads, head_dim) of a cache of E2M1 pages."""
-    device = k_cache.device
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
-        raise ValueError(f"the caches are on {device}, not on the current CUDA device")
-    if k_cache.dim() != 3 or k_cache.shape[2] % 9:
+def _fits(t, dtype, device, shape):
+    """What ``_need`` asks of one tensor, as a truth value (a call's common path:
+    its checks cost a microsecond or two, not five)."""
+    return (t.dtype is dtype and t.get_device() == device and t.shape == shape
+            and t.is_contiguous())
+
+
+def _raw_stream(stream, device):
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+
+
+def _e2m1_dims(k_cache, v_cache):
+    """(device index, num_blocks, num_kv_heads, head_dim) of caches of E2M1 pages."""
+    device = k_cache.get_device()
+    if device < 0 or device != torch._C._cuda_getDevice():
+        raise ValueError(f"the caches are on {k_cache.device}, not on the current CUDA device")
+    shape = k_cache.shape
+    if len(shape) != 3 or shape[2] % 9:
         raise ValueError("an E2M1 cache is [num_blocks, num_kv_heads, 9 * head_dim]")
-    nb, hkv, page = k_cache.shape
+    u8 = torch.uint8
+    if not (_fits(k_cache, u8, device, shape) and _fits(v_cache, u8, device, shape)):
+        _need(device, k_cache=(k_cache, u8, shape), v_cache=(v_cache, u8, shape))
+    nb, hkv, page = shape
     return device, nb, hkv, page // 9
+
+
+def _e2m1_rows(name, k_rows, v_rows, slot_mapping, k_cache, v_cache, k_scale, v_scale, error_flag,
+               stream):
+    """The write of rows into E2M1 caches, or the read of rows from them."""
+    dev, nb, hkv, d = _e2m1_dims(k_cache, v_cache)
+    dtype = k_rows.dtype
+    code = _dtype_code(dtype)
+    n = slot_mapping.numel()
+    rows = (n, hkv, d)
+    if not (_fits(k_rows, dtype, dev, rows) and _fits(v_rows, dtype, dev, rows)
+            and _fits(slot_mapping, torch.int64, dev, (n,))
+            and (error_flag is None or _fits(error_flag, torch.int32, dev, (1,)))):
+        _need(dev, k_rows=(k_rows, dtype, rows), v_rows=(v_rows, dtype, rows),
+              slot_mapping=(slot_mapping, torch.int64, (n,)),
+              error_flag=(error_flag, torch.int32, (1,)))
+    pair, cache = (k_rows.data_ptr(), v_rows.data_ptr()), (k_cache.data_ptr(), v_cache.data_ptr())
+    first, last = (pair, cache) if name == "pkv_write_e2m1" else (cache, pair)
+    status = getattr(lib(), name)(*first, slot_mapping.data_ptr(), n, *last, nb, 16, hkv, d, code,
+                                  k_scale, v_scale,
+                                  None if error_flag is None else error_flag.data_ptr(),
+                                  _raw_stream(stream, dev))
+    if status != PKV_OK:
+        raise PkvError(name, status)
 
 
 def pkv_write_e2m1(k_new, v_new, slot_mapping, k_cache, v_cache, k_scale, v_scale,
@@ -472,38 +512,16 @@ def pkv_write_e2m1(k_new, v_new, slot_mapping, k_cache, v_cache, k_scale, v_scal
     """pkv_write into 4-bit E2M1 caches (uint8 [num_blocks, Hkv, 9 D]: codes and
     block scales): slot slot_mapping[t] gets k_new[t] / k_scale and
     v_new[t] / v_scale, quantised (inputs [N, Hkv, D], fp32 or bf16)."""
-    dev, nb, hkv, d = _e2m1_dims(k_cache)
-    src = _dtype_code(k_new.dtype)
-    n = slot_mapping.numel()
-    rows = (n, hkv, d)
-    _need(dev, k_new=(k_new, k_new.dtype, rows), v_new=(v_new, k_new.dtype, rows),
-          slot_mapping=(slot_mapping, torch.int64, (n,)),
-          k_cache=(k_cache, torch.uint8, k_cache.shape),
-          v_cache=(v_cache, torch.uint8, k_cache.shape),
-          error_flag=(error_flag, torch.int32, (1,)))
-    _check("pkv_write_e2m1", lib().pkv_write_e2m1(
-        k_new.data_ptr(), v_new.data_ptr(), slot_mapping.data_ptr(), n, k_cache.data_ptr(),
-        v_cache.data_ptr(), nb, 16, hkv, d, src, float(k_scale), float(v_scale),
-        _ptr(error_flag), _stream(stream)))
+    _e2m1_rows("pkv_write_e2m1", k_new, v_new, slot_mapping, k_cache, v_cache, k_scale, v_scale,
+               error_flag, stream)
 
 
 def pkv_read_e2m1(k_cache, v_cache, slot_mapping, k_out, v_out, k_scale, v_scale,
                   error_flag=None, stream=None):
     """The values at slots slot_mapping of E2M1 caches into k_out / v_out
     ([N, Hkv, D], fp32 or bf16); rows with a negative slot keep theirs."""
-    dev, nb, hkv, d = _e2m1_dims(k_cache)
-    out = _dtype_code(k_out.dtype)
-    n = slot_mapping.numel()
-    rows = (n, hkv, d)
-    _need(dev, k_out=(k_out, k_out.dtype, rows), v_out=(v_out, k_out.dtype, rows),
-          slot_mapping=(slot_mapping, torch.int64, (n,)),
-          k_cache=(k_cache, torch.uint8, k_cache.shape),
-          v_cache=(v_cache, torch.uint8, k_cache.shape),
-          error_flag=(error_flag, torch.int32, (1,)))
-    _check("pkv_read_e2m1", lib().pkv_read_e2m1(
-        k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), n, k_out.data_ptr(),
-        v_out.data_ptr(), nb, 16, hkv, d, out, float(k_scale), float(v_scale), _ptr(error_flag),
-        _stream(stream)))
+    _e2m1_rows("pkv_read_e2m1", k_out, v_out, slot_mapping, k_cache, v_cache, k_scale, v_scale,
+               error_flag, stream)
     return k_out, v_out
 
 
@@ -514,44 +532,61 @@ def pkv_num_splits_e2m1(num_seqs, max_query_len, max_seq_len, num_q_heads, num_k
                                          int(num_q_heads), int(num_kv_heads), int(head_dim), dev))
 
 
-def _e2m1_batch(q, k_cache, v_cache, out, query_start_loc, seq_lens, block_table, max_query_len,
-                max_seq_len, num_splits, workspace, lse_out, error_flag, window):
-    """Checks of the attention's tensors; the call's dimensions, its split count
-    and its workspace.  A given workspace is passed on with the given count (0:
-    the library's own); without one, it is allocated here when needed."""
-    dev, nb, hkv, d = _e2m1_dims(k_cache)
-    if q.dim() != 3 or q.shape[2] != d:
-        raise ValueError(f"q is [num_tokens, Hq, {d}] for these caches")
-    n_tok, hq, _ = q.shape
+def _e2m1_attention(name, new, q, k_cache, v_cache, out, query_start_loc, seq_lens, block_table,
+                    max_query_len, max_seq_len, softmax_scale, k_scale, v_scale, causal,
+                    num_splits, workspace, lse_out, error_flag, stream, window):
+    """Checks the tensors and makes the call; ``new`` holds the new rows and
+    their slots for the call that writes them first.  A given workspace goes
+    with the given split count (0: the library's own); without one, it is
+    allocated here when needed."""
+    dev, nb, hkv, d = _e2m1_dims(k_cache, v_cache)
+    n_tok, hq = q.shape[0], q.shape[1] if q.dim() == 3 else 0
     seqs = seq_lens.numel()
-    if block_table.dim() != 2:
-        raise ValueError("block_table is [num_seqs, max_blocks_per_seq]")
-    width = block_table.shape[1]
-    i32 = torch.int32
-    _need(dev, q=(q, torch.bfloat16, q.shape), k_cache=(k_cache, torch.uint8, k_cache.shape),
-          v_cache=(v_cache, torch.uint8, k_cache.shape),
-          query_start_loc=(query_start_loc, i32, (seqs + 1,)), seq_lens=(seq_lens, i32, (seqs,)),
-          block_table=(block_table, i32, (seqs, width)),
-          lse_out=(lse_out, torch.float32, (n_tok, hq)), error_flag=(error_flag, i32, (1,)))
-    # (the graph runner's rows lie in pinned host memory that the device addresses)
-    if out.is_cuda or not out.is_pinned():
-        _need(dev, out=(out, torch.bfloat16, q.shape))
-    elif out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous():
-        raise ValueError("out is bf16, contiguous and of q's shape")
-    splits, ws_bytes = int(num_splits), 0
-    if workspace is None:
-        if splits == 0 and seqs > 0:
-            splits = pkv_num_splits_e2m1(seqs, max_query_len, split_span(max_seq_len, window), hq,
-                                         hkv, d, dev.index)
-        ws_bytes = pkv_workspace_bytes(seqs, hq, d, splits)
-        if ws_bytes:
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-    else:
-        if workspace.device != dev or not workspace.is_contiguous():
+    table = block_table.shape
+    width = table[1] if len(table) == 2 else 0
+    i32, bf16, rows = torch.int32, torch.bfloat16, (n_tok, hq, d)
+    # (the graph runner's output rows lie in pinned host memory that the device addresses)
+    out_dev = dev if out.is_cuda or not out.is_pinned() else -1
+    if not (_fits(q, bf16, dev, rows) and _fits(out, bf16, out_dev, rows)
+            and _fits(query_start_loc, i32, dev, (seqs + 1,)) and _fits(seq_lens, i32, dev, (seqs,))
+            and _fits(block_table, i32, dev, (seqs, width))
+            and (lse_out is None or _fits(lse_out, torch.float32, dev, (n_tok, hq)))
+            and (error_flag is None or _fits(error_flag, i32, dev, (1,)))):
+        _need(dev, q=(q, bf16, rows), query_start_loc=(query_start_loc, i32, (seqs + 1,)),
+              seq_lens=(seq_lens, i32, (seqs,)), block_table=(block_table, i32, (seqs, width)),
+              lse_out=(lse_out, torch.float32, (n_tok, hq)), error_flag=(error_flag, i32, (1,)))
+        _need(out_dev, out=(out, bf16, rows))
+    head = ()
+    if new is not None:
+        k_new, v_new, slots = new
+        rows = (n_tok, hkv, d)
+        if not (_fits(k_new, bf16, dev, rows) and _fits(v_new, bf16, dev, rows)
+                and _fits(slots, torch.int64, dev, (n_tok,))):
+            _need(dev, k_new=(k_new, bf16, rows), v_new=(v_new, bf16, rows),
+                  slot_mapping=(slots, torch.int64, (n_tok,)))
+        head = (k_new.data_ptr(), v_new.data_ptr(), slots.data_ptr())
+    ws_bytes = 0
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace is a contiguous tensor on the caches' device")
         ws_bytes = workspace.numel() * workspace.element_size()
-    return (width, seqs, n_tok, int(max_query_len), int(max_seq_len), hq, hkv, d, 16, nb, splits,
-            workspace, ws_bytes)
+    elif num_splits != 1:
+        if num_splits == 0 and seqs > 0:
+            num_splits = pkv_num_splits_e2m1(seqs, max_query_len, split_span(max_seq_len, window),
+                                             hq, hkv, d, dev)
+        ws_bytes = pkv_workspace_bytes(seqs, hq, d, num_splits)
+        if ws_bytes:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+    status = getattr(lib(), name)(
+        *head, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
+        None if lse_out is None else lse_out.data_ptr(), query_start_loc.data_ptr(),
+        seq_lens.data_ptr(), block_table.data_ptr(), width, seqs, n_tok, max_query_len,
+        max_seq_len, hq, hkv, d, 16, softmax_scale, k_scale, v_scale, 1 if causal else 0, window,
+        num_splits, None if workspace is None else workspace.data_ptr(), ws_bytes,
+        None if error_flag is None else error_flag.data_ptr(), nb, _raw_stream(stream, dev))
+    if status != PKV_OK:
+        raise PkvError(name, status)
+    return out
 
 
 def pkv_attention_varlen_e2m1(q, k_cache, v_cache, out, query_start_loc, seq_lens, block_table,
@@ -562,16 +597,10 @@ def pkv_attention_varlen_e2m1(q, k_cache, v_cache, out, query_start_loc, seq_len
     codes and block scales; q and out are bf16.  ``window`` > 0: the row at
     position p sees keys j > p - window only.  ``workspace`` as for
     pkv_attention_varlen (sized with pkv_num_splits_e2m1)."""
-    (width, seqs, n_tok, mq, ms, hq, hkv, d, bs, nb, splits, workspace, ws_bytes) = _e2m1_batch(
-        q, k_cache, v_cache, out, query_start_loc, seq_lens, block_table, max_query_len,
-        max_seq_len, num_splits, workspace, lse_out, error_flag, window)
-    _check("pkv_attention_varlen_e2m1", lib().pkv_attention_varlen_e2m1(
-        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), _ptr(lse_out),
-        query_start_loc.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), width, seqs,
-        n_tok, mq, ms, hq, hkv, d, bs, float(softmax_scale), float(k_scale), float(v_scale),
-        1 if causal else 0, int(window), splits, _ptr(workspace), ws_bytes, _ptr(error_flag), nb,
-        _stream(stream)))
-    return out
+    return _e2m1_attention("pkv_attention_varlen_e2m1", None, q, k_cache, v_cache, out,
+                           query_start_loc, seq_lens, block_table, max_query_len, max_seq_len,
+                           softmax_scale, k_scale, v_scale, causal, num_splits, workspace, lse_out,
+                           error_flag, stream, window)
 
 
 def pkv_write_attention_varlen_e2m1(k_new, v_new, slot_mapping, q, k_cache, v_cache, out,
@@ -581,20 +610,10 @@ def pkv_write_attention_varlen_e2m1(k_new, v_new, slot_mapping, q, k_cache, v_ca
                                     stream=None, window=0):
     """pkv_write_e2m1 of the bf16 k_new / v_new, then pkv_attention_varlen_e2m1,
     in one call."""
-    (width, seqs, n_tok, mq, ms, hq, hkv, d, bs, nb, splits, workspace, ws_bytes) = _e2m1_batch(
-        q, k_cache, v_cache, out, query_start_loc, seq_lens, block_table, max_query_len,
-        max_seq_len, num_splits, workspace, lse_out, error_flag, window)
-    rows = (n_tok, hkv, d)
-    _need(q.device, k_new=(k_new, torch.bfloat16, rows), v_new=(v_new, torch.bfloat16, rows),
-          slot_mapping=(slot_mapping, torch.int64, (n_tok,)))
-    _check("pkv_write_attention_varlen_e2m1", lib().pkv_write_attention_varlen_e2m1(
-        k_new.data_ptr(), v_new.data_ptr(), slot_mapping.data_ptr(), q.data_ptr(),
-        k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), _ptr(lse_out),
-        query_start_loc.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), width, seqs,
-        n_tok, mq, ms, hq, hkv, d, bs, float(softmax_scale), float(k_scale), float(v_scale),
-        1 if causal else 0, int(window), splits, _ptr(workspace), ws_bytes, _ptr(error_flag), nb,
-        _stream(stream)))
-    return out
+    return _e2m1_attention("pkv_write_attention_varlen_e2m1", (k_new, v_new, slot_mapping), q,
+                           k_cache, v_cache, out, query_start_loc, seq_lens, block_table,
+                           max_query_len, max_seq_len, softmax_scale, k_scale, v_scale, causal,
+                           num_splits, workspace, lse_out, error_flag, stream, window)
 
 
 def pkv_build_metadata(computed, scheduled, block_ids_per_request, block_size=16,

@@ -706,15 +706,13 @@ __global__ void __launch_bounds__(threads_for(KV != kKvBf16), 1)
           const uint32_t slot_base =
               smem_u32(smem + kOffKV + st * kStageBytes + part * 2 * kHalf);
           uint2 cw[kUnits];
-          uint32_t sw[kUnits / 4];                       // scale codes, four a word
+          uint32_t sc[kUnits];
 #pragma unroll
           for (int i = 0; i < kUnits; ++i) {
             const int r = r0 + i * kStep;
             const uint32_t page = slot_base + kPagesOff + (r / kBlock) * Page::kBytes;
             cw[i] = lds64(page + (r % kBlock) * Page::kRowCodes + b * (kQuant / 2));
-            const uint32_t sc =
-                lds8(page + Page::kCodes + (r % kBlock) * Page::kRowScales + b);
-            sw[i / 4] = i % 4 == 0 ? sc : sw[i / 4] | (sc << (8 * (i % 4)));
+            sc[i] = lds8(page + Page::kCodes + (r % kBlock) * Page::kRowScales + b);
           }
           uint32_t all_ok;
           asm volatile(
@@ -727,31 +725,39 @@ __global__ void __launch_bounds__(threads_for(KV != kKvBf16), 1)
             ok = false;
             break;
           }
-          const uint32_t dst = slot_base + second * kHalf + r0 * 128;
+          // chunk c0 + second of the block takes its word second, c0 + 1 - second
+          // the other
+          const uint32_t dst0 =
+              slot_base + second * kHalf + r0 * 128 + (((c0 + second) ^ r7) << 4);
+          const uint32_t dst1 =
+              slot_base + second * kHalf + r0 * 128 + (((c0 + 1 - second) ^ r7) << 4);
+          auto widen = [&](int i) {
+            const uint32_t s2 = scales2_to_f16x2(sc[i] * 0x0101u);
+            uint32_t v[4];
+            e2m1x8_to_f16x2x4(second ? cw[i].y : cw[i].x, v);
+            sts128(dst0 + i * kStep * 128, make_uint4(mul_f16x2(v[0], s2), mul_f16x2(v[1], s2),
+                                                      mul_f16x2(v[2], s2), mul_f16x2(v[3], s2)));
+            e2m1x8_to_f16x2x4(second ? cw[i].x : cw[i].y, v);
+            sts128(dst1 + i * kStep * 128, make_uint4(mul_f16x2(v[0], s2), mul_f16x2(v[1], s2),
+                                                      mul_f16x2(v[2], s2), mul_f16x2(v[3], s2)));
+          };
+          if (edge < 0 && key0 + kKeys <= kv_len) {
 #pragma unroll
-          for (int i = 0; i < kUnits; ++i) {
-            const int r = r0 + i * kStep;
-            uint4 o0 = make_uint4(0, 0, 0, 0), o1 = o0;  // key rows past the context: zero
-            uint32_t sc = (sw[i / 4] >> (8 * (i % 4))) & 0xFF;
-            bool live = key0 + r < kv_len;
-            if (part == 1 && edge >= 0 && live && (sc & 0x7F) == 0x7F) {
-              atomicOr(&notes[1 + (edge * 8 + b) * (kKeys / 32) + r / 32], 1u << (r % 32));
-              atomicOr(&notes[0], 1u);
-              live = false;
+            for (int i = 0; i < kUnits; ++i) widen(i);
+          } else {
+#pragma unroll
+            for (int i = 0; i < kUnits; ++i) {
+              const int r = r0 + i * kStep;
+              // key rows past the context, and noted blocks, become zeros
+              if (key0 + r >= kv_len) {
+                sc[i] = 0;
+              } else if (part == 1 && edge >= 0 && (sc[i] & 0x7F) == 0x7F) {
+                atomicOr(&notes[1 + (edge * 8 + b) * (kKeys / 32) + r / 32], 1u << (r % 32));
+                atomicOr(&notes[0], 1u);
+                sc[i] = 0;
+              }
+              widen(i);
             }
-            if (live) {
-              const uint32_t s2 = scales2_to_f16x2(sc * 0x0101u);
-              uint32_t v[4];
-              e2m1x8_to_f16x2x4(cw[i].x, v);
-              o0 = make_uint4(mul_f16x2(v[0], s2), mul_f16x2(v[1], s2), mul_f16x2(v[2], s2),
-                              mul_f16x2(v[3], s2));
-              e2m1x8_to_f16x2x4(cw[i].y, v);
-              o1 = make_uint4(mul_f16x2(v[0], s2), mul_f16x2(v[1], s2), mul_f16x2(v[2], s2),
-                              mul_f16x2(v[3], s2));
-            }
-            const uint32_t row = dst + i * kStep * 128;
-            sts128(row + (((c0 + second) ^ r7) << 4), second ? o1 : o0);
-            sts128(row + (((c0 + 1 - second) ^ r7) << 4), second ? o0 : o1);
           }
           // the widened tile is read by the tensor cores (async proxy)
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
