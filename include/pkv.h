@@ -45,8 +45,7 @@
  * pkv_attention_varlen and its variants _window (sliding window), _e4m3 (8-bit
  * cache), _e4m3_window, _e2m1 (4-bit cache) and _noalloc (no caller
  * workspace), pkv_write_attention_varlen / _e4m3 / _e2m1 (write and attend in
- * one call, the write folded into the decode kernel for decode steps over all
- * but E2M1 caches), pkv_cascade_splits / pkv_cascade_workspace_bytes /
+ * one call, the write folded into the decode kernel for decode steps), pkv_cascade_splits / pkv_cascade_workspace_bytes /
  * pkv_cascade_attention / _e4m3 (requests sharing a block-aligned prefix),
  * pkv_build_metadata (the step's flat-batch metadata, host only) and
  * pkv_status_string.
@@ -458,7 +457,10 @@ pkv_status pkv_attention_varlen_e2m1(const void* q, const void* k_cache, const v
 /*
  * pkv_write_attention_varlen_e2m1 - pkv_write_e2m1 (bf16 rows) then
  * pkv_attention_varlen_e2m1, as one call: every argument is checked before
- * anything is enqueued.  All num_tokens rows are stored at their slots.
+ * anything is enqueued, and the write rides in the decode kernel when every
+ * request is decode-class, as for pkv_write_attention_varlen (there, the rows
+ * of tokens at or behind query_start_loc[num_seqs], and of requests flagged
+ * PKV_FLAG_BAD_LENGTHS, are not stored).
  */
 pkv_status pkv_write_attention_varlen_e2m1(
     const void* k_new, const void* v_new, const int64_t* slot_mapping, const void* q,

@@ -49,6 +49,7 @@ using namespace pkv;
 namespace {
 
 constexpr int kMinBlocksPerSplit = 8;    // 128 keys
+constexpr int kMinBlocksPerSplitE2m1 = 32;
 constexpr int kTcMinWindow = 128;        // shortest window the tensor-core prefill takes
 constexpr int kCascadeRows = 16;         // rows per tile of the cascade prefix pass
 
@@ -206,11 +207,14 @@ int split_rule(int num_seqs, int max_query_len, int max_seq_len, int num_q_heads
   const int64_t capacity =
       static_cast<int64_t>(sms) *
       (e2m1 ? decode_e2m1_ctas_per_sm(R) : decode_ctas_per_sm(et, head_dim));
-  const int64_t target = capacity * 7 / 8;
+  // E2M1: every slot, each split at least two pairs of blocks a warp.  Two
+  // contexts of 128K keys (16 units): 19 splits take 65 us, 16 (7/8) 74, 20 (a
+  // second wave) 88.  One of 8192 keys: 16 splits 8.9 us, 33 (8 blocks each) 9.7.
+  const int64_t target = e2m1 ? capacity : capacity * 7 / 8;
   int64_t s = target / units;
   if (s <= 1) return 1;
   const int64_t nblk = (static_cast<int64_t>(max_seq_len) + kBlock - 1) / kBlock;
-  int64_t by_len = nblk / kMinBlocksPerSplit;
+  int64_t by_len = nblk / (e2m1 ? kMinBlocksPerSplitE2m1 : kMinBlocksPerSplit);
   if (by_len < 1) by_len = 1;
   if (s > by_len) s = by_len;
   if (s > kMaxSplits) s = kMaxSplits;
@@ -317,7 +321,9 @@ static pkv_status attention(const void* q, const void* k_cache, const void* v_ca
   a.num_blocks = num_blocks;
   a.k_cache = k_cache;
   a.v_cache = v_cache;
-  if (fuse_slots != nullptr && et != ElemType::kE2m1) {
+  // (E2M1: this call decides by itself whether the decode kernel stores them)
+  const bool write_first = et == ElemType::kE2m1 && max_query_len > kDecodeMaxQ;
+  if (fuse_slots != nullptr && !write_first) {
     // the step's new K/V are stored by the decode kernel (every request is
     // decode-class, checked by the caller)
     a.fuse_write = 1;
@@ -342,8 +348,7 @@ static pkv_status attention(const void* q, const void* k_cache, const void* v_ca
   a.lpt = splits == 1 && num_seqs >= 2 && num_seqs <= kLptMaxSeqs && !prefill_follows ? 1 : 0;
   cudaError_t e = cudaSuccess;
   if (et == ElemType::kE2m1) {
-    // (the write is a launch of its own: a block's scale needs 16 elements)
-    if (fuse_slots != nullptr) {
+    if (fuse_slots != nullptr && write_first) {
       const int sms = current_sms();
       if (sms <= 0) return PKV_ERR_CUDA;
       e = launch_kv_write_e2m1(fuse_k_new, fuse_v_new, true, fuse_slots, num_tokens,

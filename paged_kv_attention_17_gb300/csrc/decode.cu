@@ -380,48 +380,6 @@ __device__ __forceinline__ int64_t part_row(const AttnArgs& a, int s, int r, int
                    : ws_row(a, s, r, i, h);
 }
 
-// Longest-first dispatch of an unsplit launch (at most kLptMaxSeqs requests):
-// the request whose rank, by decreasing seq_len (ties by index), equals
-// `rank`.  After the dependency wait every CTA computes the same ranking from
-// the same seq_lens, so the ranks are a bijection onto the requests; the
-// request's query_start_loc pair and seq_len, loaded in the same round trip,
-// are returned too.  Before the wait (hint = true, L2-only loads of values
-// that may still change) the result only steers the L2 warm-up.  Keys are
-// unique (length in the high bits, reversed index in the low nine), so a
-// request's rank is the number of keys above its own.  Called by every thread.
-__device__ __forceinline__ int request_by_length_rank(const AttnArgs& a, int rank, bool hint,
-                                                      int& q0, int& q1, int& len) {
-  __shared__ uint32_t s_key[kLptMaxSeqs];
-  __shared__ int s_len[kLptMaxSeqs];
-  __shared__ int s_qsl[kLptMaxSeqs + 1];
-  __shared__ int s_pick;
-  const int n = a.num_seqs;
-  for (int i = threadIdx.x; i <= n; i += blockDim.x) {
-    s_qsl[i] = hint ? __ldcg(a.qsl + i) : __ldg(a.qsl + i);
-    if (i < n) {
-      const int L = hint ? __ldcg(a.seq_lens + i) : __ldg(a.seq_lens + i);
-      s_len[i] = L;
-      s_key[i] = (static_cast<uint32_t>(min(max(L, 0), (1 << 22) - 1)) << 9) |
-                 static_cast<uint32_t>(511 - i);
-    }
-  }
-  if (threadIdx.x == 0) s_pick = rank;     // (every rank is taken below)
-  __syncthreads();
-  for (int c = threadIdx.x; c < n; c += blockDim.x) {
-    const uint32_t kc = s_key[c];
-    int above = 0;
-    for (int j = 0; j < n; ++j) above += s_key[j] > kc ? 1 : 0;
-    if (above == rank) s_pick = c;
-  }
-  __syncthreads();
-  const int r = s_pick;
-  q0 = s_qsl[r];
-  q1 = s_qsl[r + 1];
-  len = s_len[r];
-  __syncthreads();                          // the arrays are reused by a second call
-  return r;
-}
-
 // A lane's kDPL consecutive floats of a partial row in one vector store (the
 // row is D floats and the lane's slice starts at a multiple of kDPL floats).
 template <int kDPL>

@@ -73,10 +73,9 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// 16 bytes to shared memory; bytes = 0 writes zeros and reads nothing
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
+// 16 bytes to shared memory
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -86,42 +85,34 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 template <int WORDS>
-__device__ __forceinline__ void lds_words(uint32_t (&w)[WORDS], uint32_t addr) {
+__device__ __forceinline__ void load_words(uint32_t (&w)[WORDS], const uint8_t* p) {
   if constexpr (WORDS == 4) {
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "r"(addr)
-                 : "memory");
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
   } else if constexpr (WORDS == 2) {
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                 : "=r"(w[0]), "=r"(w[1])
-                 : "r"(addr)
-                 : "memory");
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x;
+    w[1] = v.y;
   } else {
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
   }
-}
-__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
 }
 
 // p = 2^(x - ref) is kept below 2^(kSlack + kLift): the reference of a row moves
 // only when a score passes it by more than kSlack + kLift, and it is set
 // kLift below the row's maximum, so a row's largest p is at least 2^kLift and
-// f16's subnormals (below 2^-14) start 2^21 under it.
+// f16's subnormals (below 2^-14) start 2^21 under it.  A row without a score
+// yet refers to the least float: its masked p are 0, and any finite score moves it.
 constexpr float kSlack = 7.f, kLift = 7.f;
+constexpr float kNoRef = -3.402823466e38f;
 
 template <int D, int NT>
 struct Cfg {
   using P = E2m1Page<D>;
-  static constexpr int kWarps = 8;
+  static constexpr int kWarps = 6;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kRows = 8 * NT;
   static constexpr int kPair = 2;                        // blocks per stage
@@ -135,6 +126,40 @@ struct Cfg {
   static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
   static constexpr int kCtas = NT == 1 ? 2 : 1;          // per SM
 };
+
+// What a CTA does for its request: the row tile's keys [kv_lo, kv_hi), and the
+// blocks [b_beg, b_end) of its split.
+struct TileRange {
+  static constexpr int kRun = 0, kNothing = 1, kBad = 2;
+  int state, splits, kv_lo, kv_hi, b_beg, b_end;
+};
+__device__ __forceinline__ TileRange tile_range(const AttnArgs& a, int q0, int q1, int L, int split,
+                                                int rho0, int rows_per_tile) {
+  TileRange t = {TileRange::kNothing, 1, 0, 0, 0, 0};
+  const int n = q1 - q0;
+  if (n == 0) return t;
+  if (n < 0 || q0 < 0 || q1 > a.num_tokens || n > L || n > a.max_query_len ||
+      (L + kBlock - 1) / kBlock > a.max_blocks_per_seq) {
+    t.state = TileRange::kBad;
+    return t;
+  }
+  const bool decode_class = n <= kDecodeMaxQ;
+  if (!decode_class && (!a.long_rows || split > 0)) return t;   // (long requests are not split)
+  const int rows_total = a.group * n;
+  if (rho0 >= rows_total) return t;
+  const int i_first = rho0 / a.group;
+  const int i_last = (min(rho0 + rows_per_tile, rows_total) - 1) / a.group;
+  t.state = TileRange::kRun;
+  t.splits = decode_class ? a.num_splits : 1;
+  t.kv_hi = a.causal ? L - n + i_last + 1 : L;
+  t.kv_lo = a.window > 0 ? max(0, L - n + i_first - a.window + 1) : 0;
+  const int blk_lo = t.kv_lo / kBlock;
+  const int nb = (t.kv_hi + kBlock - 1) / kBlock - blk_lo;
+  const int per = (nb + t.splits - 1) / t.splits;
+  t.b_beg = blk_lo + min(nb, split * per);
+  t.b_end = blk_lo + min(nb, (split + 1) * per);
+  return t;
+}
 
 }  // namespace
 
@@ -151,44 +176,139 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, (Cfg<D, NT>::kCtas))
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g8 = lane >> 2, t4 = lane & 3;
 
+  const int kvh = static_cast<int>(blockIdx.x) % a.hkv;
+  const int split = static_cast<int>(blockIdx.x) / a.hkv;
+  const int rho0 = blockIdx.y * R;
+  int r = blockIdx.z, q0, q1, L;
   // released only after the wait: a prefill behind this grid may count on
   // every input being complete
   pdl_wait_primary();
   pdl_launch_dependents();
 
-  const int kvh = static_cast<int>(blockIdx.x) % a.hkv;
-  const int split = static_cast<int>(blockIdx.x) / a.hkv;
-  const int r = blockIdx.z;
-  const int q0 = __ldg(a.qsl + r), q1 = __ldg(a.qsl + r + 1), L = __ldg(a.seq_lens + r);
-  const int n = q1 - q0;
-  if (n == 0) return;
-  if (n < 0 || q0 < 0 || q1 > a.num_tokens || n > L || n > a.max_query_len ||
-      (L + kBlock - 1) / kBlock > a.max_blocks_per_seq) {
-    if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0)
+  if (a.lpt) {
+    r = request_by_length_rank(a, r, false, q0, q1, L);  // longest first
+  } else {
+    q0 = __ldg(a.qsl + r);
+    q1 = __ldg(a.qsl + r + 1);
+    L = __ldg(a.seq_lens + r);
+  }
+  const TileRange range = tile_range(a, q0, q1, L, split, rho0, R);
+  if (range.state != TileRange::kRun) {
+    if (range.state == TileRange::kBad && threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0)
       raise_flag(a.flag, PKV_FLAG_BAD_LENGTHS);
     return;
   }
-  const bool decode_class = n <= kDecodeMaxQ;
-  if (!decode_class && (!a.long_rows || split > 0)) return;   // (long requests are not split)
-  const int splits = decode_class ? a.num_splits : 1;
-  const int group = a.group;
+  const int group = a.group, n = q1 - q0;
   const int rows_total = group * n;
-  const int rho0 = blockIdx.y * R;
-  if (rho0 >= rows_total) return;
   const int nrows = min(R, rows_total - rho0);
   const int i_first = rho0 / group, i_last = (rho0 + nrows - 1) / group;
-  // the tile's key range, and this split's run of its blocks
-  const int kv_hi = a.causal ? L - n + i_last + 1 : L;
-  const int kv_lo = a.window > 0 ? max(0, L - n + i_first - a.window + 1) : 0;
-  const int blk_lo = kv_lo / kBlock;
-  const int nb = (kv_hi + kBlock - 1) / kBlock - blk_lo;
-  const int per = (nb + splits - 1) / splits;
-  const int b_beg = blk_lo + min(nb, split * per), b_end = blk_lo + min(nb, (split + 1) * per);
+  const int splits = range.splits;
+  const int kv_hi = range.kv_hi, kv_lo = range.kv_lo;
+  const int b_beg = range.b_beg, b_end = range.b_end;
   const int npairs = (b_end - b_beg + C::kPair - 1) / C::kPair;
   // keys every row of the tile sees: [in_lo, in_hi)
   const int in_hi = min(a.causal ? L - n + i_first + 1 : L, b_end * kBlock);
   const int in_lo = a.window > 0 ? max(0, L - n + i_last - a.window + 1) : 0;
   const int cap = min(kv_hi, b_end * kBlock);            // keys the split may see
+
+  // ---- the warp's ring: pair u = warp + k * kWarps, k = 0, 1, ... ----
+  uint8_t* const ring = smem + warp * (C::kStages * C::kStageBytes);
+  uint8_t* const ring_end = ring + C::kStages * C::kStageBytes;
+  const int32_t* table = a.block_table + static_cast<int64_t>(r) * a.max_blocks_per_seq;
+  const int npw = npairs > warp ? (npairs - warp - 1) / C::kWarps + 1 : 0;
+  const uint32_t page_stride = static_cast<uint32_t>(a.hkv) * P::kBytes;
+  const uint8_t* kbase = static_cast<const uint8_t*>(a.k_cache) + kvh * P::kBytes;
+  const uint8_t* vbase = static_cast<const uint8_t*>(a.v_cache) + kvh * P::kBytes;
+  // this lane's chunk of the scale areas: of page p = lane / kSC (K of both
+  // blocks, V of both)
+  constexpr int kSC = P::kScales / 16;
+  const bool has_scales = lane < 2 * C::kPair * kSC;
+  const uint8_t* sbase =
+      (lane / kSC < C::kPair ? kbase : vbase) + P::kCodes + (lane % kSC) * 16;
+  kbase += lane * 16;
+  vbase += lane * 16;
+  // table entries of 16 consecutive pairs of the warp, two a lane pair; 0 (a
+  // page that exists) stands for a block past the run, whose keys are masked,
+  // and for an entry outside the cache, whose rows are unspecified
+  auto load_ids = [&](int k0) -> uint32_t {
+    const int k = k0 + (lane >> 1);
+    const int blk = b_beg + C::kPair * (warp + k * C::kWarps) + (lane & 1);
+    if (k >= npw || blk >= b_end) return 0;
+    const int32_t id = __ldg(table + blk);
+    if (id < 0 || id >= a.num_blocks) {
+      raise_flag(a.flag, PKV_FLAG_BAD_BLOCK);
+      return 0;
+    }
+    return static_cast<uint32_t>(id);
+  };
+  // Fused write (decode steps): the CTA stores its KV head's rows of the new
+  // tokens among the keys it reads, a scale block (of K or of V) a thread: loaded
+  // here, stored once the pairs that hold no new token are on their way.  The
+  // other pairs are loaded after that; a second row tile of a request stores the
+  // same bytes.
+  constexpr int kNewUnits = 2 * P::kRowScales;           // scale blocks of a token's K and V row
+  static_assert(kDecodeMaxQ * kNewUnits <= C::kThreads, "a thread per scale block");
+  const int new_lo = max(L - n, max(kv_lo, b_beg * kBlock));
+  const int new_hi = a.fuse_write ? min(kv_hi, b_end * kBlock) : 0;
+  const bool stores = static_cast<int>(threadIdx.x) < (new_hi - new_lo) * kNewUnits;
+  const int new_b = threadIdx.x % P::kRowScales;
+  const bool new_v = (threadIdx.x / P::kRowScales) & 1;
+  int64_t slot = -1;
+  float x[16];
+  if (stores) {
+    const int64_t t = q0 + new_lo - (L - n) + threadIdx.x / kNewUnits;
+    slot = __ldg(a.slots + t);
+    load16(static_cast<const __nv_bfloat16*>(new_v ? a.v_new : a.k_new) + (t * a.hkv + kvh) * D +
+               new_b * kQuant,
+           x);
+  }
+  uint32_t ids = load_ids(0);
+  uint8_t* put = ring;                                   // the stage that is filled next
+  auto issue = [&](int k) {
+    if (k < npw) {
+      if ((k & 15) == 0 && k > 0) ids = load_ids(k);
+      const uint32_t to = smem_u32(put) + lane * 16;
+#pragma unroll
+      for (int j = 0; j < C::kPair; ++j) {
+        const uint64_t off = static_cast<uint64_t>(__shfl_sync(0xffffffffu, ids, 2 * (k & 15) + j)) *
+                             page_stride;
+#pragma unroll
+        for (int c = 0; c < P::kCodes / 512; ++c) {
+          cp_async16(to + j * P::kCodes + c * 512, kbase + off + c * 512);
+          cp_async16(to + (C::kPair + j) * P::kCodes + c * 512, vbase + off + c * 512);
+        }
+      }
+      const uint32_t id = __shfl_sync(0xffffffffu, ids, 2 * (k & 15) + ((lane / kSC) & 1));
+      if (has_scales)
+        cp_async16(to + C::kScaleOff, sbase + static_cast<uint64_t>(id) * page_stride);
+      put += C::kStageBytes;
+      if (put == ring_end) put = ring;
+    }
+    cp_async_commit();
+  };
+  const int early =                                      // the warp's first pair that has to wait
+      new_lo < new_hi ? (new_lo / kBlock - b_beg - C::kPair * warp) / (C::kPair * C::kWarps) : npw;
+#pragma unroll
+  for (int k = 0; k < C::kStages - 1; ++k)
+    if (k < early) issue(k);
+  if (new_lo < new_hi) {
+    if (slot >= a.num_blocks * kBlock) {                 // outside the cache: skip, report
+      raise_flag(a.flag, PKV_FLAG_BAD_SLOT);
+    } else if (slot >= 0) {                              // (negative: padding)
+      uint2 codes;
+      uint32_t scale;
+      quantise16(x, divisor(new_v ? a.wv_scale : a.wk_scale), codes, scale);
+      const int row = static_cast<int>(slot % kBlock);
+      uint8_t* page = static_cast<uint8_t*>(const_cast<void*>(new_v ? a.v_cache : a.k_cache)) +
+                      ((slot / kBlock) * a.hkv + kvh) * P::kBytes;
+      *reinterpret_cast<uint2*>(page + row * P::kRowCodes + new_b * (kQuant / 2)) = codes;
+      page[P::kCodes + row * P::kRowScales + new_b] = static_cast<uint8_t>(scale);
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int k = 0; k < C::kStages - 1; ++k)
+    if (k >= early) issue(k);
 
   // ---- this lane's q rows as f16 fragments, and its score columns' scales ----
   uint32_t qf[NT][kMT][2];
@@ -223,11 +343,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, (Cfg<D, NT>::kCtas))
     // largest |q| in [2^E, 2^(E+1)): e = E - 14 (clamped so 2^-e and 2^e are
     // normal floats; a zero row takes the lower bound)
     const int e = min(max(static_cast<int>(m16 >> 7) - 127 - 14, -100), 113);
-    const float down = __int_as_float((127 - e) << 23);
+    const float down =
+        a.scale_log2 < 0.f ? -__int_as_float((127 - e) << 23) : __int_as_float((127 - e) << 23);
 #pragma unroll
     for (int c = 0; c < kMT * 2; ++c)
       qf[nt][c >> 1][c & 1] = pack_f16x2(bf16_lo(w[c]) * down, bf16_hi(w[c]) * down);
-    const float row_sc = a.scale_log2 * __int_as_float((127 + e) << 23);
+    // (a positive score scale: its sign goes to q; at least the least normal
+    // float, so that a masked -inf stays one)
+    const float row_sc = fmaxf(fabsf(a.scale_log2) * __int_as_float((127 + e) << 23), 1.17549435e-38f);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       sc[nt][c] = __shfl_sync(0xffffffffu, row_sc, (2 * t4 + c) * 4);
@@ -236,55 +359,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, (Cfg<D, NT>::kCtas))
       low[nt][c] = a.window > 0 ? L - n + i - a.window + 1 : 0;
     }
   }
-
-  // ---- the warp's ring: pair u = warp + k * kWarps, k = 0, 1, ... ----
-  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) +
-                        warp * (C::kStages * C::kStageBytes);
-  const int32_t* table = a.block_table + static_cast<int64_t>(r) * a.max_blocks_per_seq;
-  const int npw = npairs > warp ? (npairs - warp - 1) / C::kWarps + 1 : 0;
-  const uint8_t* kbase = static_cast<const uint8_t*>(a.k_cache) + static_cast<int64_t>(kvh) * P::kBytes;
-  const uint8_t* vbase = static_cast<const uint8_t*>(a.v_cache) + static_cast<int64_t>(kvh) * P::kBytes;
-  const int64_t page_stride = static_cast<int64_t>(a.hkv) * P::kBytes;
-  // table entries of 16 consecutive pairs of the warp, two a lane pair
-  auto load_ids = [&](int k0) -> int32_t {
-    const int k = k0 + (lane >> 1);
-    const int blk = b_beg + C::kPair * (warp + k * C::kWarps) + (lane & 1);
-    if (k >= npw || blk >= b_end) return -1;
-    const int32_t id = __ldg(table + blk);
-    if (id < 0 || id >= a.num_blocks) {
-      raise_flag(a.flag, PKV_FLAG_BAD_BLOCK);
-      return -1;
-    }
-    return id;
-  };
-  int32_t ids = load_ids(0);
-  auto issue = [&](int k) {
-    if (k < npw) {
-      if ((k & 15) == 0 && k > 0) ids = load_ids(k);
-      const uint32_t st = ring + (k % C::kStages) * C::kStageBytes;
-#pragma unroll
-      for (int p = 0; p < 2 * C::kPair; ++p) {           // K of both blocks, V of both
-        const int32_t id = __shfl_sync(0xffffffffu, ids, 2 * (k & 15) + (p & 1));
-        const uint8_t* page = (p < C::kPair ? kbase : vbase) + max(id, 0) * page_stride;
-        const uint32_t bytes = id >= 0 ? 16 : 0;         // (a missing block: zeros)
-#pragma unroll
-        for (int c = 0; c < P::kCodes / 512; ++c)
-          cp_async16(st + p * P::kCodes + c * 512 + lane * 16, page + c * 512 + lane * 16, bytes);
-      }
-      // the four scale areas, kScales / 16 chunks each
-      constexpr int kSC = P::kScales / 16;
-      const int p = lane / kSC, c = lane % kSC;
-      const int32_t id = __shfl_sync(0xffffffffu, ids, 2 * (k & 15) + (p & 1));
-      if (p < 2 * C::kPair) {
-        const uint8_t* page = (p < C::kPair ? kbase : vbase) + max(id, 0) * page_stride;
-        cp_async16(st + C::kScaleOff + p * P::kScales + c * 16, page + P::kCodes + c * 16,
-                   id >= 0 ? 16 : 0);
-      }
-    }
-    cp_async_commit();
-  };
-#pragma unroll
-  for (int k = 0; k < C::kStages - 1; ++k) issue(k);
 
   const int ka = (g8 & 1) ? ((g8 >> 1) ^ 1) + 4 : g8 >> 1;   // kappa(g8); the lane's other key + 8
   const int kv[4] = {t4, (t4 ^ 1) + 4, t4 + 8, (t4 ^ 1) + 12};
@@ -298,45 +372,38 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, (Cfg<D, NT>::kCtas))
       for (int c = 0; c < 4; ++c) oacc[nt][i][c] = 0.f;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      ref[nt][c] = -INFINITY;
+      ref[nt][c] = kNoRef;
       l[nt][c] = 0.f;
     }
 #pragma unroll
     for (int c = 0; c < 4; ++c) lr[nt][c] = 0.f;
   }
 
-  for (int k = 0; k < npw; ++k) {
-    cp_async_wait<C::kStages - 2>();
-    __syncwarp();                                        // every lane's part of stage k has landed
-    issue(k + C::kStages - 1);                           // (into the stage read in step k - 1)
-    const uint32_t st = ring + (k % C::kStages) * C::kStageBytes;
-    const int key0 = (b_beg + C::kPair * (warp + k * C::kWarps)) * kBlock;
-    const bool edge = key0 + C::kPairKeys > in_hi || key0 < in_lo;
-
-    // S^T of both blocks
-    float s[C::kPair][NT][4];
+  // S^T (unscaled) of the pair in a stage
+  float s[C::kPair][NT][4];
+  auto scores = [&](const uint8_t* st, float (&x)[C::kPair][NT][4]) {
 #pragma unroll
     for (int j = 0; j < C::kPair; ++j) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) s[j][nt][c] = 0.f;
+        for (int c = 0; c < 4; ++c) x[j][nt][c] = 0.f;
       uint32_t wa[kKWords], wb[kKWords], sa[2], sb[2];
-      const uint32_t row = st + j * P::kCodes + ka * P::kRowCodes + t4 * (D / 8);
-      lds_words<kKWords>(wa, row);
-      lds_words<kKWords>(wb, row + 8 * P::kRowCodes);
-      const uint32_t srow = st + C::kScaleOff + j * P::kScales + ka * P::kRowScales + t4 * (D / 64);
+      const uint8_t* row = st + j * P::kCodes + ka * P::kRowCodes + t4 * (D / 8);
+      load_words<kKWords>(wa, row);
+      load_words<kKWords>(wb, row + 8 * P::kRowCodes);
+      const uint8_t* srow = st + C::kScaleOff + j * P::kScales + ka * P::kRowScales + t4 * (D / 64);
       if constexpr (D == 128) {
-        const uint32_t ha = scales2_to_f16x2(lds_u16(srow));
-        const uint32_t hb = scales2_to_f16x2(lds_u16(srow + 8 * P::kRowScales));
+        const uint32_t ha = scales2_to_f16x2(*reinterpret_cast<const uint16_t*>(srow));
+        const uint32_t hb =
+            scales2_to_f16x2(*reinterpret_cast<const uint16_t*>(srow + 8 * P::kRowScales));
         sa[0] = byte_perm(ha, ha, 0x1010);
         sa[1] = byte_perm(ha, ha, 0x3232);
         sb[0] = byte_perm(hb, hb, 0x1010);
         sb[1] = byte_perm(hb, hb, 0x3232);
       } else {
-        const uint32_t ca = lds_u8(srow), cb = lds_u8(srow + 8 * P::kRowScales);
-        sa[0] = sa[1] = scales2_to_f16x2(ca * 0x0101u);
-        sb[0] = sb[1] = scales2_to_f16x2(cb * 0x0101u);
+        sa[0] = sa[1] = scales2_to_f16x2(srow[0] * 0x0101u);
+        sb[0] = sb[1] = scales2_to_f16x2(srow[8 * P::kRowScales] * 0x0101u);
       }
 #pragma unroll
       for (int w = 0; w < kKWords; ++w) {
@@ -350,25 +417,89 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, (Cfg<D, NT>::kCtas))
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          mma_f16(s[j][nt], ra[0], rb[0], ra[1], rb[1], qf[nt][2 * w][0], qf[nt][2 * w][1]);
-          mma_f16(s[j][nt], ra[2], rb[2], ra[3], rb[3], qf[nt][2 * w + 1][0],
+          mma_f16(x[j][nt], ra[0], rb[0], ra[1], rb[1], qf[nt][2 * w][0], qf[nt][2 * w][1]);
+          mma_f16(x[j][nt], ra[2], rb[2], ra[3], rb[3], qf[nt][2 * w + 1][0],
                   qf[nt][2 * w + 1][1]);
         }
       }
     }
-    // scale (log2 domain) and mask
+  };
+
+  // Step k takes the scores of pair k, then its P V beside the scores of pair
+  // k + 1: one run of independent work between two branches.
+  const uint8_t* st = ring;                              // the stage of pair k
+  if (npw > 0) {
+    cp_async_wait<C::kStages - 2>();
+    __syncwarp();
+    scores(st, s);
+  }
+  for (int k = 0; k < npw; ++k) {
+    issue(k + C::kStages - 1);                           // (into the stage that step k - 1 left)
+    const int key0 = (b_beg + C::kPair * (warp + k * C::kWarps)) * kBlock;
+    const bool edge = key0 + C::kPairKeys > in_hi || key0 < in_lo;
+    // this lane's V scales: block g8 D / 128 of its four keys of both blocks
+    uint32_t cs[C::kPair][4];
 #pragma unroll
     for (int j = 0; j < C::kPair; ++j)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int c = 0; c < 4; ++c)
+        cs[j][c] = st[C::kScaleOff + (C::kPair + j) * P::kScales + kv[c] * P::kRowScales +
+                      g8 * D / 128];
+    if (edge) {
+      // p is 0 outside a row's keys, and so must p v be whatever a hidden slot
+      // holds: a scale outside the tile's keys, or a NaN one that some row of
+      // the tile may not see, counts as 0 (a 0 code times any finite scale)
+      bool bad = false;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          s[j][nt][c] *= sc[nt][c & 1];
-          if (edge) {
+      for (int j = 0; j < C::kPair; ++j) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
             const int key = key0 + j * kBlock + ka + (c >> 1) * 8;
             if (key >= lim[nt][c & 1] || key < low[nt][c & 1]) s[j][nt][c] = -INFINITY;
           }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int key = key0 + j * kBlock + kv[c];
+          const bool nan = (cs[j][c] & 0x7F) == 0x7F;
+          const bool in = key < cap && key >= kv_lo;
+          bad = bad || (nan && in);
+          if (nan || !in) cs[j][c] = 0;
+          if (nan && in) cs[j][c] = 0x100;               // remembered below
         }
+      }
+      if (__any_sync(0xffffffffu, bad)) {
+        // rows that do see such a key take the NaN in its block's dims
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int jc = 0; jc < 4 * C::kPair; ++jc) {
+            const int j = jc / 4, c = jc % 4;
+            const uint32_t v = __shfl_sync(0xffffffffu, cs[j][c], g8 * 4 + q);
+            const int key =
+                key0 + j * kBlock + ((c & 1) ? (q ^ 1) + 4 : q) + (c >> 1) * 8;
+            if (v == 0x100) {
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (key < lim[nt][e] && key >= low[nt][e]) {
+#pragma unroll
+                    for (int i = 0; i < kMT; ++i)
+                      oacc[nt][i][e] = oacc[nt][i][e + 2] = __int_as_float(0x7FC00000);
+                  }
+            }
+          }
+#pragma unroll
+        for (int jc = 0; jc < 4 * C::kPair; ++jc) cs[jc / 4][jc % 4] &= 0xFF;
+      }
+    }
+    uint32_t vs[C::kPair][2];
+#pragma unroll
+    for (int j = 0; j < C::kPair; ++j) {
+      vs[j][0] = scales2_to_f16x2(cs[j][0] | (cs[j][1] << 8));
+      vs[j][1] = scales2_to_f16x2(cs[j][2] | (cs[j][3] << 8));
+    }
     // move a row's reference when a score passes it by kSlack + kLift
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -377,6 +508,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, (Cfg<D, NT>::kCtas))
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         mx[c] = fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2]));
+        mx[c] *= sc[nt][c];
         up = up || mx[c] > ref[nt][c] + (kSlack + kLift);
       }
       if (__any_sync(0xffffffffu, up)) {
@@ -387,7 +519,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, (Cfg<D, NT>::kCtas))
             mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], o));
           if (mx[c] > ref[nt][c] + (kSlack + kLift)) {
             const float to = mx[c] - kLift;
-            const float f = ex2(ref[nt][c] - to);        // (0 from the start's -inf)
+            const float f = ex2(ref[nt][c] - to);        // (0 from kNoRef)
             ref[nt][c] = to;
             l[nt][c] *= f;
             lr[nt][c] *= f;
@@ -401,19 +533,19 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, (Cfg<D, NT>::kCtas))
         }
       }
     }
+    // every lane's part of pair k + 1 has landed
+    cp_async_wait<C::kStages - 2>();
+    __syncwarp();
     // p, its sums, and P^T operands
     uint32_t pf[C::kPair][NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float base[2];
-#pragma unroll
-      for (int c = 0; c < 2; ++c) base[c] = ref[nt][c] == -INFINITY ? 0.f : ref[nt][c];
 #pragma unroll
       for (int j = 0; j < C::kPair; ++j) {
         float p[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          p[c] = ex2(s[j][nt][c] - base[c & 1]);
+          p[c] = ex2(fmaf(s[j][nt][c], sc[nt][c & 1], -ref[nt][c & 1]));
           l[nt][c & 1] += p[c];
         }
         pf[j][nt][0] = movmatrix_t(pack_f16x2(p[0], p[1]));
@@ -423,56 +555,17 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, (Cfg<D, NT>::kCtas))
                 pf[j][nt][1]);
       }
     }
+    // (the scores of pair k + 1; past the warp's last pair, of an old stage)
+    const uint8_t* next = st + C::kStageBytes == ring_end ? ring : st + C::kStageBytes;
+    scores(next, s);
     // O^T += V^T P^T
 #pragma unroll
     for (int j = 0; j < C::kPair; ++j) {
-      const uint32_t vrow = st + (C::kPair + j) * P::kCodes + g8 * (D / 16);
-      const uint32_t srow = st + C::kScaleOff + (C::kPair + j) * P::kScales + g8 * D / 128;
-      uint32_t vw[4][kVWords], cs[4];
+      const uint8_t* vrow = st + (C::kPair + j) * P::kCodes + g8 * (D / 16);
+      uint32_t vw[4][kVWords];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        lds_words<kVWords>(vw[c], vrow + kv[c] * P::kRowCodes);
-        cs[c] = lds_u8(srow + kv[c] * P::kRowScales);
-      }
-      if (edge) {
-        // p is 0 outside a row's keys, and so must p v be whatever a hidden slot
-        // holds: a scale outside the tile's keys, or a NaN one that some row of
-        // the tile may not see, counts as 0 (a 0 code times any finite scale)
-        bool bad = false;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int key = key0 + j * kBlock + kv[c];
-          const bool nan = (cs[c] & 0x7F) == 0x7F;
-          const bool in = key < cap && key >= kv_lo;
-          bad = bad || (nan && in);
-          if (nan || !in) cs[c] = 0;
-          if (nan && in) cs[c] = 0x100;                  // remembered below
-        }
-        if (__any_sync(0xffffffffu, bad)) {
-          // rows that do see such a key take the NaN in its block's dims
-          for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const uint32_t v = __shfl_sync(0xffffffffu, cs[c], g8 * 4 + q);
-              const int key = key0 + j * kBlock + ((c & 1) ? (q ^ 1) + 4 : q) + (c >> 1) * 8;
-              if (v == 0x100) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                  for (int e = 0; e < 2; ++e)
-                    if (key < lim[nt][e] && key >= low[nt][e]) {
-#pragma unroll
-                      for (int i = 0; i < kMT; ++i)
-                        oacc[nt][i][e] = oacc[nt][i][e + 2] = __int_as_float(0x7FC00000);
-                    }
-              }
-            }
-#pragma unroll
-          for (int c = 0; c < 4; ++c) cs[c] &= 0xFF;
-        }
-      }
-      const uint32_t s01 = scales2_to_f16x2(cs[0] | (cs[1] << 8));
-      const uint32_t s23 = scales2_to_f16x2(cs[2] | (cs[3] << 8));
+      for (int c = 0; c < 4; ++c) load_words<kVWords>(vw[c], vrow + kv[c] * P::kRowCodes);
+      const uint32_t s01 = vs[j][0], s23 = vs[j][1];
 #pragma unroll
       for (int w = 0; w < kVWords; ++w) {
         // byte i of e: element 2 i of both keys of a pair; of o: element 2 i + 1
@@ -492,6 +585,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, (Cfg<D, NT>::kCtas))
         }
       }
     }
+    st = next;
     __syncwarp();                                        // the stage is read; step k + 1 refills it
   }
   cp_async_wait<0>();
@@ -515,15 +609,16 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, (Cfg<D, NT>::kCtas))
         lw[warp * R + rho] = lt;
         lrw[warp * R + rho] = lr[nt][c];
       }
+      if (rho < nrows)
 #pragma unroll
-      for (int i = 0; i < kMT; ++i)
-        *reinterpret_cast<float2*>(aw + (warp * R + rho) * D + g8 * (D / 8) + 2 * i) =
-            make_float2(oacc[nt][i][c], oacc[nt][i][c + 2]);
+        for (int i = 0; i < kMT; ++i)
+          *reinterpret_cast<float2*>(aw + (warp * R + rho) * D + g8 * (D / 8) + 2 * i) =
+              make_float2(oacc[nt][i][c], oacc[nt][i][c + 2]);
     }
   __syncthreads();
   constexpr int kDPL = D / 32;
   for (int rho = warp; rho < nrows; rho += C::kWarps) {
-    float M = -INFINITY;
+    float M = kNoRef;
 #pragma unroll
     for (int w = 0; w < C::kWarps; ++w) M = fmaxf(M, mw[w * R + rho]);
     float o[kDPL];
@@ -532,9 +627,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, (Cfg<D, NT>::kCtas))
     float lsum = 0.f, lnorm = 0.f;
 #pragma unroll
     for (int w = 0; w < C::kWarps; ++w) {
-      // (a row whose scores are all NaN keeps -inf in every warp: weight 1)
-      const float m = mw[w * R + rho];
-      const float f = m == M ? 1.f : ex2(m - M);
+      const float f = ex2(mw[w * R + rho] - M);
       lsum = fmaf(f, lw[w * R + rho], lsum);
       lnorm = fmaf(f, lrw[w * R + rho], lnorm);
       const float* src = aw + (w * R + rho) * D + lane * kDPL;

@@ -18,69 +18,6 @@
 
 namespace pkv {
 
-namespace {
-
-// A block's 16 inputs as floats.
-__device__ __forceinline__ void load16(const float* p, float (&f)[16]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 v = __ldcs(reinterpret_cast<const float4*>(p) + i);
-    f[4 * i] = v.x;
-    f[4 * i + 1] = v.y;
-    f[4 * i + 2] = v.z;
-    f[4 * i + 3] = v.w;
-  }
-}
-__device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&f)[16]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint4 w = __ldcs(reinterpret_cast<const uint4*>(p) + i);
-    f[8 * i] = bf16_lo(w.x);
-    f[8 * i + 1] = bf16_hi(w.x);
-    f[8 * i + 2] = bf16_lo(w.y);
-    f[8 * i + 3] = bf16_hi(w.y);
-    f[8 * i + 4] = bf16_lo(w.z);
-    f[8 * i + 5] = bf16_hi(w.z);
-    f[8 * i + 6] = bf16_lo(w.w);
-    f[8 * i + 7] = bf16_hi(w.w);
-  }
-}
-
-// (a, b) -> two E2M1 codes, a in the low nibble
-__device__ __forceinline__ uint32_t float2_to_e2m1x2(float a, float b) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 c;\n\tcvt.rn.satfinite.e2m1x2.f32 c, %1, %2;\n\tcvt.u32.u8 %0, c;\n\t}"
-      : "=r"(r)
-      : "f"(b), "f"(a));
-  return r;
-}
-
-__device__ __forceinline__ void quantise16(const float (&x)[16], float t, uint2& codes,
-                                           uint32_t& scale) {
-  float y[16];
-  float a = 0.f;
-  bool nan = false;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    y[i] = __fdiv_rn(x[i], t);
-    a = fmaxf(a, fabsf(y[i]));
-    nan = nan || y[i] != y[i];
-  }
-  scale = float2_to_e4m3x2(__fdiv_rn(a, 6.f), 0.f) & 0xFFu;
-  codes = make_uint2(0, 0);
-  if (nan) scale = 0x7F;
-  if (nan || scale == 0) return;
-  const float s = e4m3x2_to_float2(scale).x;
-  uint32_t c[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    c[i] = float2_to_e2m1x2(__fdiv_rn(y[2 * i], s), __fdiv_rn(y[2 * i + 1], s));
-  codes = make_uint2(c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24),
-                     c[4] | (c[5] << 8) | (c[6] << 16) | (c[7] << 24));
-}
-
-}  // namespace
-
 // One thread quantises one scale block of a token's K row and the same block
 // of its V row.
 template <typename S, int D>
@@ -91,6 +28,7 @@ __global__ void __launch_bounds__(256) kv_write_e2m1_kernel(
   using P = E2m1Page<D>;
   pdl_launch_dependents();
   pdl_wait_primary();
+  const Divisor kd = divisor(k_scale), vd = divisor(v_scale);
   const int64_t total = num_tokens * hkv * P::kRowScales;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
@@ -113,10 +51,10 @@ __global__ void __launch_bounds__(256) kv_write_e2m1_kernel(
     const int64_t sat = page + P::kCodes + row * P::kRowScales + b;
     uint2 codes;
     uint32_t scale;
-    quantise16(kf, k_scale, codes, scale);
+    quantise16(kf, kd, codes, scale);
     *reinterpret_cast<uint2*>(k_cache + at) = codes;
     k_cache[sat] = static_cast<uint8_t>(scale);
-    quantise16(vf, v_scale, codes, scale);
+    quantise16(vf, vd, codes, scale);
     *reinterpret_cast<uint2*>(v_cache + at) = codes;
     v_cache[sat] = static_cast<uint8_t>(scale);
   }

@@ -169,6 +169,26 @@ def test_write_is_bit_exact_and_touches_nothing_else(dtype, n, hkv, d, ks, vs):
     assert flag.item() == (pkv.FLAG_BAD_SLOT if n > 4 else 0)
 
 
+@pytest.mark.parametrize("t", [1.0, 0.7, 0.0123, 1.9999999, 3.0e-7, 5.5e11, 1e-30])
+def test_write_divides_correctly_everywhere(t):
+    """A million quotients of each kind: every block's scale and codes."""
+    rng = np.random.default_rng(4)
+    n, hkv, d = 1024, 8, 128
+    x = (rng.standard_normal((n, hkv, d)) * t * np.exp2(rng.integers(-12, 9, (n, hkv, 1)))).astype(np.float32)
+    x[::3, ::2] *= np.float32(0)                          # zeros of both signs
+    x[1::7, :, ::5] = -0.0
+    nb = n // 16
+    cache = torch.zeros(nb, hkv, 9 * d, dtype=torch.uint8, device=DEV)
+    other = torch.zeros_like(cache)
+    dev = torch.from_numpy(x).to(DEV)
+    pkv.pkv_write_e2m1(dev, dev, torch.arange(n, device=DEV), cache, other, t, 1.0)
+    codes, scales = e2m1.quantize(x, t)
+    want = e2m1.parts(cache.cpu().numpy(), d)
+    packed = (codes[..., 0::2] | (codes[..., 1::2] << 4)).reshape(nb, 16, hkv, d // 2).transpose(0, 2, 1, 3)
+    assert np.array_equal(want[0], packed)
+    assert np.array_equal(want[1], scales.reshape(nb, 16, hkv, d // 16).transpose(0, 2, 1, 3))
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("n, hkv, d", [(1, 1, 64), (7, 3, 64), (50, 8, 128), (700, 2, 128)])
 def test_read_is_exact(dtype, n, hkv, d):
@@ -400,6 +420,54 @@ def test_write_attend_read(lens, hq, hkv, d):
     pkv.pkv_read_e2m1(t["k"], t["v"], slots, *got, b.ks, b.vs)
     want = torch.from_numpy(e2m1.rows(b.k, new, d, b.ks)).float().bfloat16()
     assert torch.equal(got[0].cpu(), want)
+
+
+@pytest.mark.parametrize("splits", [1, 3])
+@pytest.mark.parametrize("hq, hkv, d", [(8, 2, 128), (32, 2, 64)])
+def test_the_fused_write_of_a_padded_step(hq, hkv, d, splits):
+    """Decode steps store the rows in the attention kernel: padding rows (slot -1
+    behind the last request), a slot outside the cache, blocks that begin with a
+    new token, several row tiles and splits of one request."""
+    lens = [(33, 1), (64, 4), (1, 1), (500, 2), (0, 0), (97, 3)]
+    b = Batch(lens, hq, hkv, d, seed=21)
+    rng = np.random.default_rng(22)
+    new = np.concatenate([b.slot_range(r, L - n, L) for r, (L, n) in enumerate(lens)])
+    n, pad = len(new), 3
+    kx, vx = (bf16(rng.standard_normal((n + pad, hkv, d))) for _ in range(2))
+    kx[0, 0, 3] = float("nan")                            # one row's block becomes NaN
+    t = b.dev()
+    t["q"] = torch.cat([t["q"], torch.ones(pad, hq, d, dtype=torch.bfloat16, device=DEV)])
+    slots = np.concatenate([new, np.full(pad, -1)])
+    out = torch.full_like(t["q"], 5.0)
+    lse = torch.empty(t["q"].shape[:2], device=DEV)
+    flag = torch.zeros(1, dtype=torch.int32, device=DEV)
+
+    def call(sl):
+        pkv.pkv_write_attention_varlen_e2m1(
+            kx.to(DEV), vx.to(DEV), torch.from_numpy(sl).to(DEV), t["q"], t["k"], t["v"], out, t["qsl"],
+            t["lens"], t["table"], b.mq, b.ms, b.scale, b.ks, b.vs, num_splits=splits, lse_out=lse,
+            error_flag=flag)
+
+    call(slots)
+    assert flag.item() == 0
+    b.k = e2m1.write(b.k, kx.float().numpy(), slots, b.ks)
+    b.v = e2m1.write(b.v, vx.float().numpy(), slots, b.vs)
+    assert np.array_equal(t["k"].cpu().numpy(), b.k) and np.array_equal(t["v"].cpu().numpy(), b.v)
+    assert (out[n:] == 5.0).all()
+    assert out[0, :hq // hkv].isnan().all() and not out[0, hq // hkv:].isnan().any()
+    b.k[new[0] // 16] = 0                                 # (the oracle's check leaves that request out)
+    b.v[new[0] // 16] = 0
+    o, l_ref, V, X = b.oracle()
+    got = out[1:n].float().cpu().numpy()
+    tol = 2.0 ** -8 * np.abs(o[1:]) + ((2.0 ** -10 + 2 * (d + 8) * 2.0 ** -23 * (X + 8)) * V)[1:, :, None]
+    assert (np.abs(got - o[1:]) <= tol).all()
+    # a slot outside the cache is reported, and nothing else changes
+    bad = slots.copy()
+    bad[1] = b.k.shape[0] * 16
+    before = t["k"].clone()
+    call(bad)
+    assert flag.item() == pkv.FLAG_BAD_SLOT
+    assert torch.equal(before, t["k"])
 
 
 @pytest.mark.parametrize("lens", [[(300, 1), (47, 1)], [(290, 130), (200, 1)]])
