@@ -254,13 +254,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, (Cfg<D, NT>::kCtas))
   const int new_b = threadIdx.x % P::kRowScales;
   const bool new_v = (threadIdx.x / P::kRowScales) & 1;
   int64_t slot = -1;
-  float x[16];
+  Raw16<__nv_bfloat16> raw;
   if (stores) {
     const int64_t t = q0 + new_lo - (L - n) + threadIdx.x / kNewUnits;
     slot = __ldg(a.slots + t);
-    load16(static_cast<const __nv_bfloat16*>(new_v ? a.v_new : a.k_new) + (t * a.hkv + kvh) * D +
-               new_b * kQuant,
-           x);
+    raw.load(static_cast<const __nv_bfloat16*>(new_v ? a.v_new : a.k_new) +
+             (t * a.hkv + kvh) * D + new_b * kQuant);
   }
   uint32_t ids = load_ids(0);
   uint8_t* put = ring;                                   // the stage that is filled next
@@ -297,7 +296,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, (Cfg<D, NT>::kCtas))
     } else if (slot >= 0) {                              // (negative: padding)
       uint2 codes;
       uint32_t scale;
-      quantise16(x, divisor(new_v ? a.wv_scale : a.wk_scale), codes, scale);
+      float x[16];
+      raw.floats(x);
+      const float t = new_v ? a.wv_scale : a.wk_scale;
+      quantise16(x, {t, __fdiv_rn(1.f, t)}, codes, scale);
       const int row = static_cast<int>(slot % kBlock);
       uint8_t* page = static_cast<uint8_t*>(const_cast<void*>(new_v ? a.v_cache : a.k_cache)) +
                       ((slot / kBlock) * a.hkv + kvh) * P::kBytes;

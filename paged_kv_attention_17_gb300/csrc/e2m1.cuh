@@ -64,15 +64,11 @@ __device__ __forceinline__ uint32_t byte_perm(uint32_t a, uint32_t b, uint32_t s
 // elementary functions on the IBM RISC System/6000 processor", 1990).  For t in
 // [2^-40, 2^40] no operation of it underflows where y matters: |y| < 2^-60 is a
 // code 0 whatever its last bit.  Taking the remainder as q t - x keeps the sign
-// of a zero x.  Blocks with a y beyond 1e30, an infinity or a NaN are left to the
-// plain division.
+// of a zero x.  Other t, and blocks with a y beyond 1e30, an infinity or a NaN,
+// are left to the plain division.
 struct Divisor {
-  float t, inv;
-  bool plain;
+  float t, inv;                                          // inv: RN32(1 / t)
 };
-__device__ __forceinline__ Divisor divisor(float t) {
-  return {t, __fdiv_rn(1.f, t), !(t >= 0x1p-40f && t <= 0x1p40f)};
-}
 __device__ __forceinline__ float quotient_step(float q, float x, float t, float inv) {
   return fmaf(-fmaf(q, t, -x), inv, q);
 }
@@ -83,31 +79,31 @@ __device__ __forceinline__ float max_abs_nan(float a, float b) {
   return d;
 }
 
-// A block's 16 inputs as floats.
-__device__ __forceinline__ void load16(const float* p, float (&f)[16]) {
+// A block's 16 inputs, as loaded and as floats.
+template <typename S>
+struct Raw16 {
+  uint4 w[static_cast<int>(sizeof(S))];
+  __device__ __forceinline__ void load(const S* p) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 v = __ldcs(reinterpret_cast<const float4*>(p) + i);
-    f[4 * i] = v.x;
-    f[4 * i + 1] = v.y;
-    f[4 * i + 2] = v.z;
-    f[4 * i + 3] = v.w;
+    for (int i = 0; i < static_cast<int>(sizeof(S)); ++i)
+      w[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
   }
-}
-__device__ __forceinline__ void load16(const __nv_bfloat16* p, float (&f)[16]) {
+  __device__ __forceinline__ void floats(float (&f)[16]) const {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint4 w = __ldcs(reinterpret_cast<const uint4*>(p) + i);
-    f[8 * i] = bf16_lo(w.x);
-    f[8 * i + 1] = bf16_hi(w.x);
-    f[8 * i + 2] = bf16_lo(w.y);
-    f[8 * i + 3] = bf16_hi(w.y);
-    f[8 * i + 4] = bf16_lo(w.z);
-    f[8 * i + 5] = bf16_hi(w.z);
-    f[8 * i + 6] = bf16_lo(w.w);
-    f[8 * i + 7] = bf16_hi(w.w);
+    for (int i = 0; i < static_cast<int>(sizeof(S)); ++i) {
+      const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if constexpr (sizeof(S) == 4) {
+          f[4 * i + k] = __uint_as_float(v[k]);
+        } else {
+          f[8 * i + 2 * k] = bf16_lo(v[k]);
+          f[8 * i + 2 * k + 1] = bf16_hi(v[k]);
+        }
+      }
+    }
   }
-}
+};
 
 // (a, b) -> two E2M1 codes, a in the low nibble
 __device__ __forceinline__ uint32_t float2_to_e2m1x2(float a, float b) {
@@ -116,6 +112,22 @@ __device__ __forceinline__ uint32_t float2_to_e2m1x2(float a, float b) {
       : "=r"(r)
       : "f"(b), "f"(a));
   return r;
+}
+
+// The definition with plain divisions (a call: rare, and kept out of the
+// registers of the common path).
+static __device__ __noinline__ uint3 quantise16_plain(const float* x, float t) {
+  float a = 0.f;
+  for (int i = 0; i < 16; ++i) a = max_abs_nan(a, __fdiv_rn(x[i], t));
+  if (a != a) return make_uint3(0, 0, 0x7F);             // a NaN among the 16
+  const uint32_t scale = float2_to_e4m3x2(__fdiv_rn(a, 6.f), 0.f) & 0xFFu;
+  uint32_t c[2] = {0, 0};
+  const float s = e4m3x2_to_float2(scale).x;
+  for (int i = 0; i < 16 && scale != 0; i += 2)
+    c[i / 8] |= float2_to_e2m1x2(__fdiv_rn(__fdiv_rn(x[i], t), s),
+                                 __fdiv_rn(__fdiv_rn(x[i + 1], t), s))
+                << (4 * (i % 8));
+  return make_uint3(c[0], c[1], scale);
 }
 
 __device__ __forceinline__ void quantise16(const float (&x)[16], const Divisor& d, uint2& codes,
@@ -128,32 +140,31 @@ __device__ __forceinline__ void quantise16(const float (&x)[16], const Divisor& 
     y[i] = quotient_step(q, x[i], d.t, d.inv);
     a = max_abs_nan(a, y[i]);
   }
-  const bool plain = d.plain || !(a <= 1e30f);
-  if (plain) {
-    a = 0.f;
+  if (!(a <= 1e30f) || !(d.t >= 0x1p-40f && d.t <= 0x1p40f)) {
+    float copy[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      y[i] = __fdiv_rn(x[i], d.t);
-      a = max_abs_nan(a, y[i]);
-    }
+    for (int i = 0; i < 16; ++i) copy[i] = x[i];
+    const uint3 r = quantise16_plain(copy, d.t);
+    codes = make_uint2(r.x, r.y);
+    scale = r.z;
+    return;
   }
+  // Quotients by 6 and by s, divisors of at most four significant bits: such a
+  // quotient is at least 2^-29 (relative) from every midpoint of two floats, so
+  // one step, whose error before its last rounding is below 2^-43 even from an
+  // approximate reciprocal (2^-22), rounds correctly.
+  constexpr float kInv6 = 1.f / 6.f;
+  scale = float2_to_e4m3x2(quotient_step(a * kInv6, a, 6.f, kInv6), 0.f) & 0xFFu;
   codes = make_uint2(0, 0);
-  scale = 0x7F;                                          // a NaN among the 16: its block's scale
-  if (a != a) return;
-  scale = float2_to_e4m3x2(__fdiv_rn(a, 6.f), 0.f) & 0xFFu;
   if (scale == 0) return;
-  // Quotients by s, of four significant bits: y / s is at least 2^-29 (relative)
-  // from every midpoint of two floats, so one step, whose error before its last
-  // rounding is about 2^-46, rounds correctly.
-  const float s = e4m3x2_to_float2(scale).x, inv = __fdiv_rn(1.f, s);
+  const float s = e4m3x2_to_float2(scale).x;
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
   uint32_t c[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float y0 = y[2 * i], y1 = y[2 * i + 1];
-    const float z0 = plain ? __fdiv_rn(y0, s) : quotient_step(y0 * inv, y0, s, inv);
-    const float z1 = plain ? __fdiv_rn(y1, s) : quotient_step(y1 * inv, y1, s, inv);
-    c[i] = float2_to_e2m1x2(z0, z1);
-  }
+  for (int i = 0; i < 8; ++i)
+    c[i] = float2_to_e2m1x2(quotient_step(y[2 * i] * inv, y[2 * i], s, inv),
+                            quotient_step(y[2 * i + 1] * inv, y[2 * i + 1], s, inv));
   codes = make_uint2(c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24),
                      c[4] | (c[5] << 8) | (c[6] << 16) | (c[7] << 24));
 }

@@ -18,67 +18,68 @@
 
 namespace pkv {
 
-// One thread quantises one scale block of a token's K row and the same block
-// of its V row.
-template <typename S, int D>
-__global__ void __launch_bounds__(256) kv_write_e2m1_kernel(
+// One thread quantises one scale block of a token's K row, or of its V row, with
+// its next block's inputs on their way.  Index is the type of the flat unit index:
+// 32 bits where they hold it (its divisions are the address arithmetic).
+template <typename S, int D, typename Index>
+__global__ void __launch_bounds__(256, sizeof(S) == 2 ? 4 : 3) kv_write_e2m1_kernel(
     const S* __restrict__ k_new, const S* __restrict__ v_new, const int64_t* __restrict__ slots,
-    int64_t num_tokens, uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache,
-    int64_t num_slots, int hkv, float k_scale, float v_scale, int32_t* flag) {
+    Index units, uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache, int64_t num_slots,
+    int hkv, Divisor k_scale, Divisor v_scale, int32_t* flag) {
   using P = E2m1Page<D>;
   pdl_launch_dependents();
   pdl_wait_primary();
-  const Divisor kd = divisor(k_scale), vd = divisor(v_scale);
-  const int64_t total = num_tokens * hkv * P::kRowScales;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-       i += stride) {
-    const int b = static_cast<int>(i % P::kRowScales);
-    const int64_t th = i / P::kRowScales;
-    const int h = static_cast<int>(th % hkv);
-    const int64_t slot = __ldg(slots + th / hkv);
-    float kf[16], vf[16];
-    load16(k_new + i * kQuant, kf);
-    load16(v_new + i * kQuant, vf);
-    if (slot < 0) continue;                 // padding token: nothing to write
-    if (slot >= num_slots) {                // outside the cache: skip, report
+  const Index stride = static_cast<Index>(gridDim.x) * 256;
+  Index i = static_cast<Index>(blockIdx.x) * 256 + threadIdx.x;   // K's units, then V's
+  Raw16<S> raw;
+  int64_t slot = -1;
+  auto fetch = [&](Index u) {
+    const bool is_v = u >= units;
+    if (is_v) u -= units;
+    slot = __ldg(slots + u / P::kRowScales / hkv);
+    raw.load((is_v ? v_new : k_new) + static_cast<int64_t>(u) * kQuant);
+  };
+  if (i < 2 * units) fetch(i);
+  for (; i < 2 * units; i += stride) {
+    float x[16];
+    raw.floats(x);
+    const int64_t to = slot;
+    if (i + stride < 2 * units) fetch(i + stride);
+    const bool is_v = i >= units;
+    const Index u = is_v ? i - units : i;
+    const int b = static_cast<int>(u % P::kRowScales);
+    const int h = static_cast<int>(u / P::kRowScales % hkv);
+    if (to < 0) continue;                   // padding token: nothing to write
+    if (to >= num_slots) {                  // outside the cache: skip, report
       if (b == 0 && h == 0) raise_flag(flag, PKV_FLAG_BAD_SLOT);
       continue;
     }
-    const int row = static_cast<int>(slot % kBlock);
-    const int64_t page = ((slot / kBlock) * hkv + h) * P::kBytes;
-    const int64_t at = page + row * P::kRowCodes + b * (kQuant / 2);
-    const int64_t sat = page + P::kCodes + row * P::kRowScales + b;
     uint2 codes;
     uint32_t scale;
-    quantise16(kf, kd, codes, scale);
-    *reinterpret_cast<uint2*>(k_cache + at) = codes;
-    k_cache[sat] = static_cast<uint8_t>(scale);
-    quantise16(vf, vd, codes, scale);
-    *reinterpret_cast<uint2*>(v_cache + at) = codes;
-    v_cache[sat] = static_cast<uint8_t>(scale);
+    quantise16(x, is_v ? v_scale : k_scale, codes, scale);
+    const int row = static_cast<int>(to % kBlock);
+    uint8_t* page = (is_v ? v_cache : k_cache) + ((to / kBlock) * hkv + h) * P::kBytes;
+    *reinterpret_cast<uint2*>(page + row * P::kRowCodes + b * (kQuant / 2)) = codes;
+    page[P::kCodes + row * P::kRowScales + b] = static_cast<uint8_t>(scale);
   }
 }
 
-// One thread widens the 16 bytes of output (8 bf16 or 4 fp32 elements) of a K
-// row and the same of its V row, so a warp's stores are contiguous.
-template <typename O, int D>
+// One thread widens 16 bytes of output (8 bf16 or 4 fp32 elements) of a K row and
+// the same of its V row, so a warp's stores are contiguous.  Index as above.
+template <typename O, int D, typename Index>
 __global__ void __launch_bounds__(256) kv_read_e2m1_kernel(
     const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ v_cache,
-    const int64_t* __restrict__ slots, int64_t num_rows, O* __restrict__ k_out,
-    O* __restrict__ v_out, int64_t num_slots, int hkv, float k_scale, float v_scale,
-    int32_t* flag) {
+    const int64_t* __restrict__ slots, Index units, O* __restrict__ k_out, O* __restrict__ v_out,
+    int64_t num_slots, int hkv, float k_scale, float v_scale, int32_t* flag) {
   using P = E2m1Page<D>;
   constexpr int kPer = 16 / static_cast<int>(sizeof(O));
-  constexpr int kRow = D / kPer;                         // threads per (row, head)
+  constexpr int kRow = D / kPer;                         // units of a (row, head)
   pdl_launch_dependents();
   pdl_wait_primary();
-  const int64_t total = num_rows * hkv * kRow;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-       i += stride) {
+  const Index stride = static_cast<Index>(gridDim.x) * 256;
+  for (Index i = static_cast<Index>(blockIdx.x) * 256 + threadIdx.x; i < units; i += stride) {
     const int c = static_cast<int>(i % kRow);
-    const int64_t th = i / kRow;
+    const Index th = i / kRow;
     const int h = static_cast<int>(th % hkv);
     const int64_t slot = __ldg(slots + th / hkv);
     if (slot < 0) continue;                 // padding row: left as it is
@@ -92,9 +93,9 @@ __global__ void __launch_bounds__(256) kv_read_e2m1_kernel(
     const int64_t sat = page + P::kCodes + row * P::kRowScales + c * kPer / kQuant;
     auto widen = [&](const uint8_t* cache, float t, O* out) {
       uint32_t w;
-      if constexpr (kPer == 8) w = *reinterpret_cast<const uint32_t*>(cache + at);
-      else w = *reinterpret_cast<const uint16_t*>(cache + at);
-      const float s = e4m3x2_to_float2(cache[sat]).x;
+      if constexpr (kPer == 8) w = __ldg(reinterpret_cast<const uint32_t*>(cache + at));
+      else w = __ldg(reinterpret_cast<const uint16_t*>(cache + at));
+      const float s = e4m3x2_to_float2(__ldg(cache + sat)).x;
       uint32_t r[4];
       e2m1x8_to_f16x2x4(w, r);
       float f[kPer];
@@ -114,23 +115,20 @@ __global__ void __launch_bounds__(256) kv_read_e2m1_kernel(
         o = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
                        __float_as_uint(f[3]));
       }
-      __stcs(reinterpret_cast<uint4*>(out + i * kPer), o);
+      __stcs(reinterpret_cast<uint4*>(out + static_cast<int64_t>(i) * kPer), o);
     };
     widen(k_cache, k_scale, k_out);
     widen(v_cache, v_scale, v_out);
   }
 }
 
-static cudaLaunchConfig_t row_config(int64_t total, int num_sms, cudaStream_t stream,
-                                     cudaLaunchAttribute* attr) {
-  const int threads = 256;
-  int64_t blocks = (total + threads - 1) / threads;
-  const int64_t cap = static_cast<int64_t>(num_sms) * 8;
-  if (blocks > cap) blocks = cap;
-  if (blocks < 1) blocks = 1;
+// `per_sm` resident CTAs an SM at most, striding over the units.
+static cudaLaunchConfig_t unit_config(int64_t units, int num_sms, int per_sm, cudaStream_t stream,
+                                      cudaLaunchAttribute* attr) {
+  const int64_t blocks = (units + 255) / 256, cap = static_cast<int64_t>(num_sms) * per_sm;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-  cfg.blockDim = dim3(threads);
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks < cap ? blocks : cap));
+  cfg.blockDim = dim3(256);
   cfg.stream = stream;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -138,19 +136,28 @@ static cudaLaunchConfig_t row_config(int64_t total, int num_sms, cudaStream_t st
   cfg.numAttrs = 1;
   return cfg;
 }
+// (with room for a stride past the end: at most 2^21 threads)
+static bool fits_32(int64_t units) { return units < (int64_t{1} << 31); }
 
 template <typename S, int D>
 static cudaError_t launch_write_t(const void* k_new, const void* v_new, const int64_t* slots,
                                   int64_t num_tokens, void* k_cache, void* v_cache,
                                   int64_t num_slots, int hkv, float k_scale, float v_scale,
                                   int32_t* flag, int num_sms, cudaStream_t stream) {
+  const int64_t units = num_tokens * hkv * E2m1Page<D>::kRowScales;
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg =
-      row_config(num_tokens * hkv * E2m1Page<D>::kRowScales, num_sms, stream, attr);
-  return cudaLaunchKernelEx(&cfg, kv_write_e2m1_kernel<S, D>, static_cast<const S*>(k_new),
-                            static_cast<const S*>(v_new), slots, num_tokens,
-                            static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache),
-                            num_slots, hkv, k_scale, v_scale, flag);
+      unit_config(2 * units, num_sms, sizeof(S) == 2 ? 4 : 3, stream, attr);
+  auto go = [&](auto index) {
+    using Index = decltype(index);
+    return cudaLaunchKernelEx(&cfg, kv_write_e2m1_kernel<S, D, Index>,
+                              static_cast<const S*>(k_new), static_cast<const S*>(v_new), slots,
+                              static_cast<Index>(units), static_cast<uint8_t*>(k_cache),
+                              static_cast<uint8_t*>(v_cache), num_slots, hkv,
+                              Divisor{k_scale, 1.f / k_scale}, Divisor{v_scale, 1.f / v_scale},
+                              flag);
+  };
+  return fits_32(2 * units) ? go(uint32_t{0}) : go(uint64_t{0});
 }
 
 cudaError_t launch_kv_write_e2m1(const void* k_new, const void* v_new, bool src_bf16,
@@ -169,16 +176,20 @@ cudaError_t launch_kv_write_e2m1(const void* k_new, const void* v_new, bool src_
 template <typename O, int D>
 static cudaError_t launch_read_t(const void* k_cache, const void* v_cache, const int64_t* slots,
                                  int64_t num_rows, void* k_out, void* v_out, int64_t num_slots,
-                                 int hkv, float k_scale, float v_scale, int32_t* flag,
-                                 int num_sms, cudaStream_t stream) {
+                                 int hkv, float k_scale, float v_scale, int32_t* flag, int num_sms,
+                                 cudaStream_t stream) {
+  const int64_t units = num_rows * hkv * (D / (16 / static_cast<int>(sizeof(O))));
   cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg = row_config(
-      num_rows * hkv * (D / (16 / static_cast<int>(sizeof(O)))), num_sms, stream, attr);
-  return cudaLaunchKernelEx(&cfg, kv_read_e2m1_kernel<O, D>,
-                            static_cast<const uint8_t*>(k_cache),
-                            static_cast<const uint8_t*>(v_cache), slots, num_rows,
-                            static_cast<O*>(k_out), static_cast<O*>(v_out), num_slots, hkv,
-                            k_scale, v_scale, flag);
+  const cudaLaunchConfig_t cfg = unit_config(units, num_sms, 8, stream, attr);
+  auto go = [&](auto index) {
+    using Index = decltype(index);
+    return cudaLaunchKernelEx(&cfg, kv_read_e2m1_kernel<O, D, Index>,
+                              static_cast<const uint8_t*>(k_cache),
+                              static_cast<const uint8_t*>(v_cache), slots,
+                              static_cast<Index>(units), static_cast<O*>(k_out),
+                              static_cast<O*>(v_out), num_slots, hkv, k_scale, v_scale, flag);
+  };
+  return fits_32(units) ? go(uint32_t{0}) : go(uint64_t{0});
 }
 
 cudaError_t launch_kv_read_e2m1(const void* k_cache, const void* v_cache, const int64_t* slots,
