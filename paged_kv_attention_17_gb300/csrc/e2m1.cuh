@@ -72,10 +72,36 @@ struct Divisor {
 __device__ __forceinline__ float quotient_step(float q, float x, float t, float inv) {
   return fmaf(-fmaf(q, t, -x), inv, q);
 }
-// max(a, |b|), NaN if either is
-__device__ __forceinline__ float max_abs_nan(float a, float b) {
+// The same on two quotients at once, from nx = -x and ninv = -inv: q0 = nx ninv,
+// then q + (q t + nx) ninv.
+typedef unsigned long long Pair;
+__device__ __forceinline__ Pair pair_of(float lo, float hi) {
+  Pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 halves(Pair v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ Pair pair_mul(Pair a, Pair b) {
+  Pair d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ Pair pair_fma(Pair a, Pair b, Pair c) {
+  Pair d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ Pair quotient_step(Pair q, Pair nx, Pair t, Pair ninv) {
+  return pair_fma(pair_fma(q, t, nx), ninv, q);
+}
+// max(a, |b|, |c|), NaN if any is
+__device__ __forceinline__ float max_abs_nan(float a, float b, float c) {
   float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(fabsf(b)));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
   return d;
 }
 
@@ -118,7 +144,8 @@ __device__ __forceinline__ uint32_t float2_to_e2m1x2(float a, float b) {
 // registers of the common path).
 static __device__ __noinline__ uint3 quantise16_plain(const float* x, float t) {
   float a = 0.f;
-  for (int i = 0; i < 16; ++i) a = max_abs_nan(a, __fdiv_rn(x[i], t));
+  for (int i = 0; i < 16; i += 2)
+    a = max_abs_nan(a, __fdiv_rn(x[i], t), __fdiv_rn(x[i + 1], t));
   if (a != a) return make_uint3(0, 0, 0x7F);             // a NaN among the 16
   const uint32_t scale = float2_to_e4m3x2(__fdiv_rn(a, 6.f), 0.f) & 0xFFu;
   uint32_t c[2] = {0, 0};
@@ -132,13 +159,16 @@ static __device__ __noinline__ uint3 quantise16_plain(const float* x, float t) {
 
 __device__ __forceinline__ void quantise16(const float (&x)[16], const Divisor& d, uint2& codes,
                                            uint32_t& scale) {
-  float y[16];
+  const Pair t2 = pair_of(d.t, d.t), ninv2 = pair_of(-d.inv, -d.inv), minus = pair_of(-1.f, -1.f);
+  Pair y[8];
   float a = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float q = quotient_step(x[i] * d.inv, x[i], d.t, d.inv);
-    y[i] = quotient_step(q, x[i], d.t, d.inv);
-    a = max_abs_nan(a, y[i]);
+  for (int i = 0; i < 8; ++i) {
+    const Pair nx = pair_of(-x[2 * i], -x[2 * i + 1]);
+    y[i] = quotient_step(pair_mul(nx, ninv2), nx, t2, ninv2);
+    y[i] = quotient_step(y[i], nx, t2, ninv2);
+    const float2 v = halves(y[i]);
+    a = max_abs_nan(a, v.x, v.y);
   }
   if (!(a <= 1e30f) || !(d.t >= 0x1p-40f && d.t <= 0x1p40f)) {
     float copy[16];
@@ -160,11 +190,14 @@ __device__ __forceinline__ void quantise16(const float (&x)[16], const Divisor& 
   const float s = e4m3x2_to_float2(scale).x;
   float inv;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  const Pair s2 = pair_of(s, s), nis2 = pair_of(-inv, -inv);
   uint32_t c[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    c[i] = float2_to_e2m1x2(quotient_step(y[2 * i] * inv, y[2 * i], s, inv),
-                            quotient_step(y[2 * i + 1] * inv, y[2 * i + 1], s, inv));
+  for (int i = 0; i < 8; ++i) {
+    const Pair ny = pair_mul(y[i], minus);
+    const float2 z = halves(quotient_step(pair_mul(ny, nis2), ny, s2, nis2));
+    c[i] = float2_to_e2m1x2(z.x, z.y);
+  }
   codes = make_uint2(c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24),
                      c[4] | (c[5] << 8) | (c[6] << 16) | (c[7] << 24));
 }
