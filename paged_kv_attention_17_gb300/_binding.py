@@ -1,19 +1,22 @@
 """ctypes binding of ``libpkv.so`` (the C ABI declared in ``include/pkv.h``).
 
 Argument marshalling only: each wrapper reads pointers, shapes and the current
-CUDA stream from torch tensors and calls the C entry point of the same name;
-every step of the computation runs in the library's CUDA kernels.  There is no
+CUDA stream from torch tensors and calls the C entry point of the same name
+(the E2M1 ones through ``_calls.so``, which reads and checks the tensors in
+compiled code); every step of the computation runs in the library's CUDA kernels.  There is no
 fallback: if the library is missing or a call fails, an exception is raised.
 """
 
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "libpkv.so")
+_CALLS_PATH = os.path.join(os.path.dirname(_LIB_PATH), "_calls.so")
 _lib = None
 
 PKV_OK = 0
@@ -440,69 +443,44 @@ def pkv_cascade_attention(q, k_cache, v_cache, out, query_start_loc, suffix_lens
     return out
 
 
-def _need(device, **tensors):
-    """Raise unless each named (tensor, dtype, shape) is a contiguous tensor of
-    that dtype and shape on CUDA device ``device``; an entry whose tensor is
-    None is skipped."""
-    for name, (t, dtype, shape) in tensors.items():
-        if t is None:
-            continue
-        if t.dtype != dtype:
-            raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
-        if t.get_device() != device:
-            raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
-        if t.shape != shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+_calls = None
+_address = {}
 
 
-def _fits(t, dtype, device, shape):
-    """What ``_need`` asks of one tensor, as a truth value (a call's common path:
-    its checks cost a microsecond or two, not five)."""
-    return (t.dtype is dtype and t.get_device() == device and t.shape == shape
-            and t.is_contiguous())
+def _load_calls():
+    """The compiled argument checks (``csrc/calls.cpp``), and the addresses of the
+    library functions that they call."""
+    global _calls
+    if not os.path.exists(_CALLS_PATH):
+        raise ImportError(f"not built: {_CALLS_PATH} is missing "
+                          "(run paged_kv_attention_17_gb300.build.build())")
+    for name in ("pkv_write_e2m1", "pkv_read_e2m1", "pkv_attention_varlen_e2m1",
+                 "pkv_write_attention_varlen_e2m1"):
+        _address[name] = ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value
+    spec = importlib.util.spec_from_file_location("_calls", _CALLS_PATH)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    _calls = module
+    return module
 
 
-def _raw_stream(stream, device):
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
-
-
-def _e2m1_dims(k_cache, v_cache):
-    """(device index, num_blocks, num_kv_heads, head_dim) of caches of E2M1 pages."""
-    device = k_cache.get_device()
-    if device < 0 or device != torch._C._cuda_getDevice():
-        raise ValueError(f"the caches are on {k_cache.device}, not on the current CUDA device")
-    shape = k_cache.shape
-    if len(shape) != 3 or shape[2] % 9:
-        raise ValueError("an E2M1 cache is [num_blocks, num_kv_heads, 9 * head_dim]")
-    u8 = torch.uint8
-    if not (_fits(k_cache, u8, device, shape) and _fits(v_cache, u8, device, shape)):
-        _need(device, k_cache=(k_cache, u8, shape), v_cache=(v_cache, u8, shape))
-    nb, hkv, page = shape
-    return device, nb, hkv, page // 9
+def _device_and_stream(cache, stream):
+    """The current device, which the cache has to be on, and the call's stream."""
+    if not cache.is_cuda:
+        raise ValueError("the caches are not on a CUDA device")
+    device = torch._C._cuda_getDevice()
+    if stream is None:
+        return device, torch._C._cuda_getCurrentRawStream(device)
+    return device, stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _e2m1_rows(name, k_rows, v_rows, slot_mapping, k_cache, v_cache, k_scale, v_scale, error_flag,
                stream):
     """The write of rows into E2M1 caches, or the read of rows from them."""
-    dev, nb, hkv, d = _e2m1_dims(k_cache, v_cache)
-    dtype = k_rows.dtype
-    code = _dtype_code(dtype)
-    n = slot_mapping.numel()
-    rows = (n, hkv, d)
-    if not (_fits(k_rows, dtype, dev, rows) and _fits(v_rows, dtype, dev, rows)
-            and _fits(slot_mapping, torch.int64, dev, (n,))
-            and (error_flag is None or _fits(error_flag, torch.int32, dev, (1,)))):
-        _need(dev, k_rows=(k_rows, dtype, rows), v_rows=(v_rows, dtype, rows),
-              slot_mapping=(slot_mapping, torch.int64, (n,)),
-              error_flag=(error_flag, torch.int32, (1,)))
-    pair, cache = (k_rows.data_ptr(), v_rows.data_ptr()), (k_cache.data_ptr(), v_cache.data_ptr())
-    first, last = (pair, cache) if name == "pkv_write_e2m1" else (cache, pair)
-    status = getattr(lib(), name)(*first, slot_mapping.data_ptr(), n, *last, nb, 16, hkv, d, code,
-                                  k_scale, v_scale,
-                                  None if error_flag is None else error_flag.data_ptr(),
-                                  _raw_stream(stream, dev))
+    calls = _calls or _load_calls()
+    device, raw = _device_and_stream(k_cache, stream)
+    status = calls.rows(_address[name], name == "pkv_write_e2m1", k_rows, v_rows, slot_mapping,
+                        k_cache, v_cache, k_scale, v_scale, error_flag, device, raw)
     if status != PKV_OK:
         raise PkvError(name, status)
 
@@ -532,58 +510,26 @@ def pkv_num_splits_e2m1(num_seqs, max_query_len, max_seq_len, num_q_heads, num_k
                                          int(num_q_heads), int(num_kv_heads), int(head_dim), dev))
 
 
-def _e2m1_attention(name, new, q, k_cache, v_cache, out, query_start_loc, seq_lens, block_table,
-                    max_query_len, max_seq_len, softmax_scale, k_scale, v_scale, causal,
-                    num_splits, workspace, lse_out, error_flag, stream, window):
-    """Checks the tensors and makes the call; ``new`` holds the new rows and
-    their slots for the call that writes them first.  A given workspace goes
-    with the given split count (0: the library's own); without one, it is
-    allocated here when needed."""
-    dev, nb, hkv, d = _e2m1_dims(k_cache, v_cache)
-    n_tok, hq = q.shape[0], q.shape[1] if q.dim() == 3 else 0
-    seqs = seq_lens.numel()
-    table = block_table.shape
-    width = table[1] if len(table) == 2 else 0
-    i32, bf16, rows = torch.int32, torch.bfloat16, (n_tok, hq, d)
-    # (the graph runner's output rows lie in pinned host memory that the device addresses)
-    out_dev = dev if out.is_cuda or not out.is_pinned() else -1
-    if not (_fits(q, bf16, dev, rows) and _fits(out, bf16, out_dev, rows)
-            and _fits(query_start_loc, i32, dev, (seqs + 1,)) and _fits(seq_lens, i32, dev, (seqs,))
-            and _fits(block_table, i32, dev, (seqs, width))
-            and (lse_out is None or _fits(lse_out, torch.float32, dev, (n_tok, hq)))
-            and (error_flag is None or _fits(error_flag, i32, dev, (1,)))):
-        _need(dev, q=(q, bf16, rows), query_start_loc=(query_start_loc, i32, (seqs + 1,)),
-              seq_lens=(seq_lens, i32, (seqs,)), block_table=(block_table, i32, (seqs, width)),
-              lse_out=(lse_out, torch.float32, (n_tok, hq)), error_flag=(error_flag, i32, (1,)))
-        _need(out_dev, out=(out, bf16, rows))
-    head = ()
-    if new is not None:
-        k_new, v_new, slots = new
-        rows = (n_tok, hkv, d)
-        if not (_fits(k_new, bf16, dev, rows) and _fits(v_new, bf16, dev, rows)
-                and _fits(slots, torch.int64, dev, (n_tok,))):
-            _need(dev, k_new=(k_new, bf16, rows), v_new=(v_new, bf16, rows),
-                  slot_mapping=(slots, torch.int64, (n_tok,)))
-        head = (k_new.data_ptr(), v_new.data_ptr(), slots.data_ptr())
-    ws_bytes = 0
-    if workspace is not None:
-        if workspace.get_device() != dev or not workspace.is_contiguous():
-            raise ValueError("workspace is a contiguous tensor on the caches' device")
-        ws_bytes = workspace.numel() * workspace.element_size()
-    elif num_splits != 1:
+def _e2m1_attention(name, k_new, v_new, slots, q, k_cache, v_cache, out, query_start_loc,
+                    seq_lens, block_table, max_query_len, max_seq_len, softmax_scale, k_scale,
+                    v_scale, causal, num_splits, workspace, lse_out, error_flag, stream, window):
+    """The attention call, after a write of new rows where there are any.  A
+    given workspace goes with the given split count (0: the library's own);
+    without one, it is allocated here when needed."""
+    calls = _calls or _load_calls()
+    device, raw = _device_and_stream(k_cache, stream)
+    if workspace is None and num_splits != 1 and q.dim() == 3 and k_cache.dim() == 3:
+        seqs, (_, hq, d) = seq_lens.numel(), q.shape
         if num_splits == 0 and seqs > 0:
             num_splits = pkv_num_splits_e2m1(seqs, max_query_len, split_span(max_seq_len, window),
-                                             hq, hkv, d, dev)
-        ws_bytes = pkv_workspace_bytes(seqs, hq, d, num_splits)
-        if ws_bytes:
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-    status = getattr(lib(), name)(
-        *head, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
-        None if lse_out is None else lse_out.data_ptr(), query_start_loc.data_ptr(),
-        seq_lens.data_ptr(), block_table.data_ptr(), width, seqs, n_tok, max_query_len,
-        max_seq_len, hq, hkv, d, 16, softmax_scale, k_scale, v_scale, 1 if causal else 0, window,
-        num_splits, None if workspace is None else workspace.data_ptr(), ws_bytes,
-        None if error_flag is None else error_flag.data_ptr(), nb, _raw_stream(stream, dev))
+                                             hq, k_cache.shape[1], d, device)
+        nbytes = pkv_workspace_bytes(seqs, hq, d, num_splits)
+        if nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=k_cache.device)
+    status = calls.attention(_address[name], k_new, v_new, slots, q, k_cache, v_cache, out,
+                             query_start_loc, seq_lens, block_table, max_query_len, max_seq_len,
+                             softmax_scale, k_scale, v_scale, causal, num_splits, workspace,
+                             lse_out, error_flag, window, device, raw)
     if status != PKV_OK:
         raise PkvError(name, status)
     return out
@@ -597,8 +543,8 @@ def pkv_attention_varlen_e2m1(q, k_cache, v_cache, out, query_start_loc, seq_len
     codes and block scales; q and out are bf16.  ``window`` > 0: the row at
     position p sees keys j > p - window only.  ``workspace`` as for
     pkv_attention_varlen (sized with pkv_num_splits_e2m1)."""
-    return _e2m1_attention("pkv_attention_varlen_e2m1", None, q, k_cache, v_cache, out,
-                           query_start_loc, seq_lens, block_table, max_query_len, max_seq_len,
+    return _e2m1_attention("pkv_attention_varlen_e2m1", None, None, None, q, k_cache, v_cache,
+                           out, query_start_loc, seq_lens, block_table, max_query_len, max_seq_len,
                            softmax_scale, k_scale, v_scale, causal, num_splits, workspace, lse_out,
                            error_flag, stream, window)
 
@@ -610,7 +556,7 @@ def pkv_write_attention_varlen_e2m1(k_new, v_new, slot_mapping, q, k_cache, v_ca
                                     stream=None, window=0):
     """pkv_write_e2m1 of the bf16 k_new / v_new, then pkv_attention_varlen_e2m1,
     in one call."""
-    return _e2m1_attention("pkv_write_attention_varlen_e2m1", (k_new, v_new, slot_mapping), q,
+    return _e2m1_attention("pkv_write_attention_varlen_e2m1", k_new, v_new, slot_mapping, q,
                            k_cache, v_cache, out, query_start_loc, seq_lens, block_table,
                            max_query_len, max_seq_len, softmax_scale, k_scale, v_scale, causal,
                            num_splits, workspace, lse_out, error_flag, stream, window)
