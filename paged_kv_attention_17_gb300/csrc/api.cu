@@ -195,9 +195,10 @@ int split_rule(int num_seqs, int max_query_len, int max_seq_len, int num_q_heads
   const int sms = device_sms(device);
   if (sms <= 0) return 0;
   const int group = num_q_heads / num_kv_heads;
-  const int qd = max_query_len < kDecodeMaxQ ? (max_query_len < 1 ? 1 : max_query_len) : kDecodeMaxQ;
   const bool e2m1 = et == ElemType::kE2m1;
-  const int R = e2m1 ? decode_e2m1_rows_per_tile(group, qd, false)
+  const int qmax = max_query_len < 1 ? 1 : max_query_len;
+  const int qd = qmax <= kDecodeMaxQ ? qmax : (e2m1 ? 1 : kDecodeMaxQ);
+  const int R = e2m1 ? decode_e2m1_rows_per_tile(group, qmax, false)
                      : decode_rows_per_tile(group, qd, false);
   const int64_t units = static_cast<int64_t>(num_seqs) * num_kv_heads * ((group * qd + R - 1) / R);
   // decode CTA slots of the device (two per SM for the tensor-core build);

@@ -112,7 +112,7 @@ constexpr float kNoRef = -3.402823466e38f;
 template <int D, int NT>
 struct Cfg {
   using P = E2m1Page<D>;
-  static constexpr int kWarps = 6;
+  static constexpr int kWarps = NT == 1 ? 6 : 8;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kRows = 8 * NT;
   static constexpr int kPair = 2;                        // blocks per stage
@@ -694,10 +694,14 @@ static cudaError_t launch_t(const AttnArgs& a, int row_tiles, cudaStream_t strea
   return cudaLaunchKernelEx(&cfg, decode_e2m1_kernel<D, NT>, a);
 }
 
-// Rows per tile: 8 where no request's rows exceed them, else 16 (a tile's
-// cached rows are read once for all of its rows).
+// Rows per tile: 8 where that holds a request's rows, else 16 (a tile's cached rows
+// are read once for all of its rows).  Beside requests that the prefill kernel
+// takes (max_query_len above the decode bound, no long_rows), the decode rows
+// are taken to be single tokens, as such batches have them.
 int decode_e2m1_rows_per_tile(int group, int max_query_len, bool long_rows) {
-  const int64_t q = long_rows ? max_query_len : (max_query_len < kDecodeMaxQ ? max_query_len : kDecodeMaxQ);
+  const int64_t q = long_rows                     ? max_query_len
+                    : max_query_len > kDecodeMaxQ ? 1
+                                                  : max_query_len;
   return group * (q < 1 ? 1 : q) <= 8 ? 8 : 16;
 }
 
