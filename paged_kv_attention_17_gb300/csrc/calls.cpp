@@ -28,12 +28,18 @@ const Tensor* tensor(PyObject* o, const char* name) {
   return &THPVariable_Unpack(o);
 }
 
-// A contiguous tensor of that type and shape on CUDA device `device`.
+// Memory that the kernels may address: on the device, or pinned on the host (as the
+// graph runner's staging and output rows are).
+bool reachable(const Tensor& t, int device) {
+  return t.get_device() == device || (t.device().is_cpu() && t.is_pinned());
+}
+
+// A contiguous, reachable tensor of that type and shape.
 bool fits(const Tensor& t, const char* name, at::ScalarType type, int device,
           std::initializer_list<int64_t> shape) {
   if (t.scalar_type() != type)
     return fail(PyExc_TypeError, "%s has the wrong dtype for this call", name);
-  if (t.get_device() != device)
+  if (!reachable(t, device))
     return fail(PyExc_ValueError, "%s is not on the device of the caches", name);
   if (t.sizes() != at::IntArrayRef(shape.begin(), shape.size()))
     return fail(PyExc_ValueError, "%s has the wrong shape for this call", name);
@@ -68,6 +74,7 @@ bool caches(PyObject* k, PyObject* v, int device, Caches* c) {
                 "k_cache");
   *c = {kt->data_ptr(), vt->data_ptr(), device, kt->size(0), kt->size(1), kt->size(2) / 9};
   const int64_t page = kt->size(2);
+  if (!vt->is_cuda()) return fail(PyExc_ValueError, "%s is not on a CUDA device", "v_cache");
   return fits(*kt, "k_cache", at::kByte, device, {c->blocks, c->heads, page}) &&
          fits(*vt, "v_cache", at::kByte, device, {c->blocks, c->heads, page});
 }
@@ -160,11 +167,9 @@ PyObject* attention(PyObject* const* a, Py_ssize_t n) {
   if (table->dim() != 2)
     return PyErr_Format(PyExc_ValueError, "block_table is [num_seqs, max_blocks_per_seq]");
   const int64_t tokens = q->size(0), hq = q->size(1), seqs = lens->numel(), width = table->size(1);
-  // (the graph runner's output rows lie in pinned host memory that the device addresses)
-  const int out_device = out->is_cuda() || !out->is_pinned() ? c.device : -1;
   void *lse, *flag;
   if (!fits(*q, "q", at::kBFloat16, c.device, {tokens, hq, c.dim}) ||
-      !fits(*out, "out", at::kBFloat16, out_device, {tokens, hq, c.dim}) ||
+      !fits(*out, "out", at::kBFloat16, c.device, {tokens, hq, c.dim}) ||
       !fits(*qsl, "query_start_loc", at::kInt, c.device, {seqs + 1}) ||
       !fits(*lens, "seq_lens", at::kInt, c.device, {seqs}) ||
       !fits(*table, "block_table", at::kInt, c.device, {seqs, width}) ||

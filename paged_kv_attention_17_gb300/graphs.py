@@ -16,7 +16,8 @@ one graph holding a whole decode step on static buffers:
 2.-3. ``pkv_write_attention_varlen``: the new tokens' K/V stored by the decode
    kernel itself, then attention (one query token per request),
 
-(``pkv_write_attention_varlen_e4m3`` over an 8-bit E4M3 cache),
+(``pkv_write_attention_varlen_e4m3`` over an 8-bit E4M3 cache,
+``pkv_write_attention_varlen_e2m1`` over a 4-bit E2M1 one),
 4. the output rows back to pinned host memory.
 
 How step 1 and 4 are done (``inputs``):
@@ -122,7 +123,7 @@ class DecodeGraphRunner:
 
     k_cache, v_cache: device [num_blocks, 16, hkv, D] (bf16 or fp32, or uint8
     E4M3 codes with ``kv_scales`` = (k_scale, v_scale) and bf16 q / new K/V /
-    out), used in place.  max_seq_len bounds every request's context (it sizes the split
+    out; or uint8 E2M1 pages [num_blocks, hkv, 9 D], likewise), used in place.  max_seq_len bounds every request's context (it sizes the split
     count at capture).  The output of a step stays valid in the returned host
     tensor until its staging slot is reused (``slots`` steps later).
     inputs: "stage" (default), "mapped" or "memcpy" - how the packed inputs
@@ -139,14 +140,22 @@ class DecodeGraphRunner:
         self.inputs = inputs
         self.k_cache, self.v_cache = k_cache, v_cache
         self.device = k_cache.device
-        self.e4m3 = k_cache.dtype == torch.uint8
-        if self.e4m3 and kv_scales is None:
-            raise ValueError("an E4M3 (uint8) cache needs kv_scales=(k_scale, v_scale)")
-        self.kv_scales = tuple(float(x) for x in kv_scales) if self.e4m3 else None
-        self.dtype = torch.bfloat16 if self.e4m3 else k_cache.dtype   # q / new K/V / out
-        _, bs, self.hkv, self.d = k_cache.shape
-        if bs != 16:
-            raise ValueError("block size must be 16")
+        codes = k_cache.dtype == torch.uint8
+        self.e2m1 = codes and k_cache.dim() == 3
+        self.e4m3 = codes and not self.e2m1
+        if codes and kv_scales is None:
+            raise ValueError("an E4M3 or E2M1 (uint8) cache needs kv_scales=(k_scale, v_scale)")
+        self.kv_scales = tuple(float(x) for x in kv_scales) if codes else None
+        self.dtype = torch.bfloat16 if codes else k_cache.dtype   # q / new K/V / out
+        if self.e2m1:
+            _, self.hkv, page = k_cache.shape
+            if page % 9:
+                raise ValueError("an E2M1 cache is [num_blocks, hkv, 9 * D]")
+            self.d = page // 9
+        else:
+            _, bs, self.hkv, self.d = k_cache.shape
+            if bs != 16:
+                raise ValueError("block size must be 16")
         self.hq = int(num_q_heads)
         self.scale = float(softmax_scale)
         self.max_blocks = int(max_blocks_per_seq)
@@ -168,7 +177,8 @@ class DecodeGraphRunner:
                          for _ in range(slots)]
         self.flag = torch.zeros(1, dtype=torch.int32, device=dev)
         self.host_flag = [torch.zeros(1, dtype=torch.int32).pin_memory() for _ in range(slots)]
-        self.splits = {b: B.pkv_num_splits(b, 1, self.max_seq_len, self.hq, self.hkv, self.d,
+        num_splits = B.pkv_num_splits_e2m1 if self.e2m1 else B.pkv_num_splits
+        self.splits = {b: num_splits(b, 1, self.max_seq_len, self.hq, self.hkv, self.d,
                                            dev.index) for b in self.sizes}
         ws = max(B.pkv_workspace_bytes(b, self.hq, self.d, self.splits[b]) for b in self.sizes)
         self.workspace = torch.zeros(max(ws, 256), dtype=torch.uint8, device=dev)
@@ -213,7 +223,15 @@ class DecodeGraphRunner:
             out = self.out[:b]
             self.flag.zero_()
             self.dev_in[:lay.nbytes].copy_(self.host_in[slot][:lay.nbytes], non_blocking=True)
-        if self.e4m3:
+        if self.e2m1:
+            ks, vs = self.kv_scales
+            B.pkv_write_attention_varlen_e2m1(v["k_new"], v["v_new"], v["slot_mapping"], v["q"],
+                                              self.k_cache, self.v_cache, out,
+                                              v["query_start_loc"], v["seq_lens"],
+                                              v["block_table"], 1, self.max_seq_len, self.scale,
+                                              ks, vs, causal=True, num_splits=self.splits[b],
+                                              workspace=self.workspace, error_flag=self.flag)
+        elif self.e4m3:
             ks, vs = self.kv_scales
             B.pkv_write_attention_varlen_e4m3(v["k_new"], v["v_new"], v["slot_mapping"], v["q"],
                                               self.k_cache, self.v_cache, out,

@@ -504,6 +504,52 @@ def test_captured_and_replayed_on_another_stream(lens):
     assert flag.item() == 0
 
 
+@pytest.mark.parametrize("inputs", ["stage", "mapped", "memcpy"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_graph_runner_steps(inputs, d):
+    """Steps of several sizes through one runner: new rows in the cache bit-exact,
+    outputs as the oracle's, padding untouched."""
+    from paged_kv_attention_17_gb300.graphs import DecodeGraphRunner
+    hq, hkv = 8, 2
+    lens = [(40, 1), (1, 1), (700, 1), (17, 1), (128, 1)]
+    b = Batch(lens, hq, hkv, d, seed=30)
+    t = b.dev()
+    runner = DecodeGraphRunner(t["k"], t["v"], hq, b.scale, b.width, 16 * b.width, max_batch=8,
+                               sizes=[1, 4, 8], inputs=inputs, kv_scales=(b.ks, b.vs))
+    rng = np.random.default_rng(31)
+    for pick in ([0, 1, 2, 3, 4], [2], [4, 1, 0], [3, 2, 1, 0]):
+        step = runner.begin(len(pick))
+        kx, vx = (bf16(rng.standard_normal((len(pick), hkv, d))) for _ in range(2))
+        slots = np.array([b.slot_range(r, b.lens[r][0] - 1, b.lens[r][0])[0] for r in pick])
+        step.q.copy_(b.q[pick])
+        step.k_new.copy_(kx)
+        step.v_new.copy_(vx)
+        step.slot_mapping.copy_(torch.from_numpy(slots))
+        step.seq_lens.copy_(torch.from_numpy(b.seq_lens[pick]))
+        step.block_table.copy_(torch.from_numpy(np.maximum(b.table[pick], 0)))
+        runner.launch(step)
+        out, flag = runner.result(step)
+        assert flag == 0
+        b.k = e2m1.write(b.k, kx.float().numpy(), slots, b.ks)
+        b.v = e2m1.write(b.v, vx.float().numpy(), slots, b.vs)
+        assert np.array_equal(t["k"].cpu().numpy(), b.k)
+        assert np.array_equal(t["v"].cpu().numpy(), b.v)
+        o, _, V, X = b.oracle()
+        rel = (d + 8) * 2.0 ** -23 * (X + 8)
+        tol = 2.0 ** -8 * np.abs(o) + ((2.0 ** -10 + 2 * rel + b.ms * 2.0 ** -32) * V)[..., None]
+        assert (np.abs(out.float().numpy() - o[pick]) <= tol[pick]).all()
+
+
+def test_the_runner_refuses_a_cache_without_scales_or_of_another_shape():
+    from paged_kv_attention_17_gb300.graphs import DecodeGraphRunner
+    cache = torch.zeros(4, 2, 9 * 64, dtype=torch.uint8, device=DEV)
+    with pytest.raises(ValueError):
+        DecodeGraphRunner(cache, cache.clone(), 4, 0.1, 4, 64, max_batch=1)
+    bad = torch.zeros(4, 2, 9 * 64 + 1, dtype=torch.uint8, device=DEV)
+    with pytest.raises(ValueError):
+        DecodeGraphRunner(bad, bad.clone(), 4, 0.1, 4, 64, max_batch=1, kv_scales=(1.0, 1.0))
+
+
 def test_bindings_refuse_wrong_tensors():
     b = Batch([(30, 1), (40, 1)], 4, 2, 128, seed=20)
     t = b.dev()
