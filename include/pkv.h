@@ -227,8 +227,13 @@ int pkv_num_splits(int num_seqs, int max_query_len, int max_seq_len, int num_q_h
                    int num_kv_heads, int head_dim, int device);
 
 /*
- * pkv_num_splits_e2m1 - the same for pkv_attention_varlen_e2m1: its own count,
- * as its tiles hold 8 or 16 rows.  The same bounds.
+ * pkv_num_splits_e2m1 - the same for pkv_attention_varlen_e2m1, whose tiles hold
+ * 8 or 16 rows and whose CTAs run one or two to an SM: U units as above (one
+ * decode token a request where max_query_len > PKV_DECODE_MAX_QLEN), B blocks of
+ * max_seq_len, s = min(B / 8, 7/8 SMs / U); where that leaves a split more than 64
+ * blocks, s = min(CTA slots / U, max(s, B / 32)); at most 64, and 1 where the
+ * split would not save B (s - 1) / s >= 48 blocks.  Returns 0 for invalid
+ * arguments or device.
  */
 int pkv_num_splits_e2m1(int num_seqs, int max_query_len, int max_seq_len, int num_q_heads,
                         int num_kv_heads, int head_dim, int device);

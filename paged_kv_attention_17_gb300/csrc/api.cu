@@ -2,6 +2,7 @@
 // heuristic, workspace sizing, TMA descriptor encoding and kernel launches.
 // Every entry point only enqueues work on the caller's stream: no allocation,
 // no synchronisation, no host read of device data.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <cudaTypedefs.h>
@@ -28,7 +29,7 @@ cudaError_t launch_kv_read_e2m1(const void* k_cache, const void* v_cache, const 
                                 int64_t num_rows, void* k_out, void* v_out, bool out_bf16,
                                 int64_t num_slots, int hkv, int head_dim, float k_scale,
                                 float v_scale, int32_t* flag, int num_sms, cudaStream_t stream);
-cudaError_t launch_decode_e2m1(const AttnArgs& a, int head_dim, cudaStream_t stream);
+cudaError_t launch_decode_e2m1(const AttnArgs& a, int head_dim, int num_sms, cudaStream_t stream);
 int decode_e2m1_rows_per_tile(int group, int max_query_len, bool long_rows);
 int decode_e2m1_ctas_per_sm(int rows_per_tile);
 cudaError_t launch_decode(const AttnArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
@@ -49,7 +50,6 @@ using namespace pkv;
 namespace {
 
 constexpr int kMinBlocksPerSplit = 8;    // 128 keys
-constexpr int kMinBlocksPerSplitE2m1 = 32;
 constexpr int kTcMinWindow = 128;        // shortest window the tensor-core prefill takes
 constexpr int kCascadeRows = 16;         // rows per tile of the cascade prefix pass
 
@@ -184,6 +184,23 @@ bool valid_dtype(pkv_dtype dt) { return dt == PKV_F32 || dt == PKV_BF16; }
 
 bool valid_scale(float s) { return std::isfinite(s) && s > 0.f; }
 
+// The E2M1 split rule.  A warp takes about 1 us a pair of blocks and the combine
+// costs about 2.5 us, so a split has to save about three pairs a warp.  CTAs (of 8
+// warps) on 7/8 of the SMs are best while that leaves a split at most 64 blocks;
+// longer runs take both CTA slots of every SM, at least 32 blocks a split.
+// Measured, us (splits): one request over 8 KV heads, 1024 keys 8.5 (1), 6.7 (8);
+// 2048 keys 13.1 (1), 8.4 (4), 6.8 (16); 8192 keys 8.9 (16), 9.1 (19), 9.7 (33);
+// 8192 keys at head_dim 64 7.7 (16), 8.9 (19); 32768 keys 16.8 (16), 15.7 (38); two
+// of 128K keys 74 (16), 65 (19, every slot), 88 (20, a second wave).
+int split_rule_e2m1(int64_t units, int64_t nblk, int sms, int64_t capacity) {
+  constexpr int kWarps = 8;
+  int64_t s = std::min<int64_t>(nblk / kMinBlocksPerSplit, sms * 7 / 8 / units);
+  s = std::max<int64_t>(s, 1);
+  if (nblk > 64 * s) s = std::min(capacity / units, std::max(s, nblk / 32));
+  s = std::min<int64_t>(s, kMaxSplits);
+  return s > 1 && nblk * (s - 1) >= 3 * 2 * kWarps * s ? static_cast<int>(s) : 1;
+}
+
 // The split rule for a cache type: as many splits as fit in 7/8 of the
 // device's decode CTA slots in one wave (none when the grid is already nearly
 // full), every split keeping at least kMinBlocksPerSplit blocks.
@@ -208,14 +225,12 @@ int split_rule(int num_seqs, int max_query_len, int max_seq_len, int num_q_heads
   const int64_t capacity =
       static_cast<int64_t>(sms) *
       (e2m1 ? decode_e2m1_ctas_per_sm(R) : decode_ctas_per_sm(et, head_dim));
-  // E2M1: every slot, each split at least two pairs of blocks a warp.  Two
-  // contexts of 128K keys (16 units): 19 splits take 65 us, 16 (7/8) 74, 20 (a
-  // second wave) 88.  One of 8192 keys: 16 splits 8.9 us, 33 (8 blocks each) 9.7.
-  const int64_t target = e2m1 ? capacity : capacity * 7 / 8;
+  const int64_t nblk = (static_cast<int64_t>(max_seq_len) + kBlock - 1) / kBlock;
+  if (e2m1) return split_rule_e2m1(units, nblk, sms, capacity);
+  const int64_t target = capacity * 7 / 8;
   int64_t s = target / units;
   if (s <= 1) return 1;
-  const int64_t nblk = (static_cast<int64_t>(max_seq_len) + kBlock - 1) / kBlock;
-  int64_t by_len = nblk / (e2m1 ? kMinBlocksPerSplitE2m1 : kMinBlocksPerSplit);
+  int64_t by_len = nblk / kMinBlocksPerSplit;
   if (by_len < 1) by_len = 1;
   if (s > by_len) s = by_len;
   if (s > kMaxSplits) s = kMaxSplits;
@@ -349,14 +364,14 @@ static pkv_status attention(const void* q, const void* k_cache, const void* v_ca
   a.lpt = splits == 1 && num_seqs >= 2 && num_seqs <= kLptMaxSeqs && !prefill_follows ? 1 : 0;
   cudaError_t e = cudaSuccess;
   if (et == ElemType::kE2m1) {
+    const int sms = current_sms();
+    if (sms <= 0) return PKV_ERR_CUDA;
     if (fuse_slots != nullptr && write_first) {
-      const int sms = current_sms();
-      if (sms <= 0) return PKV_ERR_CUDA;
       e = launch_kv_write_e2m1(fuse_k_new, fuse_v_new, true, fuse_slots, num_tokens,
                                const_cast<void*>(k_cache), const_cast<void*>(v_cache), num_slots,
                                num_kv_heads, head_dim, k_scale, v_scale, error_flag, sms, st);
     }
-    if (e == cudaSuccess) e = launch_decode_e2m1(a, head_dim, st);
+    if (e == cudaSuccess) e = launch_decode_e2m1(a, head_dim, sms, st);
   } else {
     e = launch_decode(a, kmap, vmap, et, head_dim, /*pdl=*/true, st);
   }

@@ -31,6 +31,7 @@
 //   kappa(2 q) = q, kappa(2 q + 1) = (q ^ 1) + 4 makes the transposed score
 //   fragment (movmatrix) the P^T operand of those V keys, keeps K's row loads
 //   free of bank conflicts, and V's at two ways.
+#include <atomic>
 #include <cmath>
 
 #include "e2m1.cuh"
@@ -109,10 +110,10 @@ __device__ __forceinline__ void load_words(uint32_t (&w)[WORDS], const uint8_t* 
 constexpr float kSlack = 7.f, kLift = 7.f;
 constexpr float kNoRef = -3.402823466e38f;
 
-template <int D, int NT>
+template <int D, int NT, int W>
 struct Cfg {
   using P = E2m1Page<D>;
-  static constexpr int kWarps = NT == 1 ? 6 : 8;
+  static constexpr int kWarps = W;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kRows = 8 * NT;
   static constexpr int kPair = 2;                        // blocks per stage
@@ -124,8 +125,14 @@ struct Cfg {
   static constexpr int kRing = kWarps * kStages * kStageBytes;
   static constexpr int kMerge = kWarps * kRows * (D + 3) * 4;
   static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
-  static constexpr int kCtas = NT == 1 ? 2 : 1;          // per SM
+  static constexpr int kCtas = W <= 6 ? 2 : 1;           // per SM
 };
+
+// Where a merge row keeps its 16-byte chunks: position = chunk ^ this.
+template <int D>
+__device__ __forceinline__ int chunk_swizzle(int row) {
+  return D == 128 ? (row >> 1) & 3 : ((row >> 1) & 1) | ((row & 4));
+}
 
 // What a CTA does for its request: the row tile's keys [kv_lo, kv_hi), and the
 // blocks [b_beg, b_end) of its split.
@@ -163,10 +170,10 @@ __device__ __forceinline__ TileRange tile_range(const AttnArgs& a, int q0, int q
 
 }  // namespace
 
-template <int D, int NT>
-__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, (Cfg<D, NT>::kCtas))
+template <int D, int NT, int W>
+__global__ void __launch_bounds__(Cfg<D, NT, W>::kThreads, (Cfg<D, NT, W>::kCtas))
     decode_e2m1_kernel(const AttnArgs a) {
-  using C = Cfg<D, NT>;
+  using C = Cfg<D, NT, W>;
   using P = E2m1Page<D>;
   constexpr int kKWords = D / 32;                        // code words of a lane's K row part
   constexpr int kVWords = D / 64;                        // code words of a lane's V row part
@@ -611,11 +618,16 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, (Cfg<D, NT>::kCtas))
         lw[warp * R + rho] = lt;
         lrw[warp * R + rho] = lr[nt][c];
       }
-      if (rho < nrows)
+      // 16-byte chunks of the row, permuted so that the 8 lanes of a store phase
+      // (two g8, four rows) hit distinct banks
+      if (rho < nrows) {
+        float4* row = reinterpret_cast<float4*>(aw + (warp * R + rho) * D);
 #pragma unroll
-        for (int i = 0; i < kMT; ++i)
-          *reinterpret_cast<float2*>(aw + (warp * R + rho) * D + g8 * (D / 8) + 2 * i) =
-              make_float2(oacc[nt][i][c], oacc[nt][i][c + 2]);
+        for (int i = 0; i < kMT; i += 2)
+          row[(g8 * (D / 32) + i / 2) ^ chunk_swizzle<D>(rho)] =
+              make_float4(oacc[nt][i][c], oacc[nt][i][c + 2], oacc[nt][i + 1][c],
+                          oacc[nt][i + 1][c + 2]);
+      }
     }
   __syncthreads();
   constexpr int kDPL = D / 32;
@@ -632,7 +644,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, (Cfg<D, NT>::kCtas))
       const float f = ex2(mw[w * R + rho] - M);
       lsum = fmaf(f, lw[w * R + rho], lsum);
       lnorm = fmaf(f, lrw[w * R + rho], lnorm);
-      const float* src = aw + (w * R + rho) * D + lane * kDPL;
+      const int chunk = (lane * kDPL / 4) ^ chunk_swizzle<D>(rho);
+      const float* src = aw + (w * R + rho) * D + chunk * 4 + lane * kDPL % 4;
 #pragma unroll
       for (int e = 0; e < kDPL; ++e) o[e] = fmaf(f, src[e], o[e]);
     }
@@ -664,21 +677,21 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, (Cfg<D, NT>::kCtas))
   }
 }
 
-template <int D, int NT>
+template <int D, int NT, int W>
 static cudaError_t launch_t(const AttnArgs& a, int row_tiles, cudaStream_t stream) {
-  using C = Cfg<D, NT>;
-  static unsigned done = 0;                              // one bit per device already configured
+  using C = Cfg<D, NT, W>;
+  static std::atomic<unsigned> done{0};                  // one bit per device already configured
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 32 || !((done >> dev) & 1u)) {
-    e = cudaFuncSetAttribute(decode_e2m1_kernel<D, NT>,
+    e = cudaFuncSetAttribute(decode_e2m1_kernel<D, NT, W>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(decode_e2m1_kernel<D, NT>,
+      e = cudaFuncSetAttribute(decode_e2m1_kernel<D, NT, W>,
                                cudaFuncAttributePreferredSharedMemoryCarveout, 100);
     if (e != cudaSuccess) return e;
-    if (dev < 32) done |= 1u << dev;
+    if (dev < 32) done.fetch_or(1u << dev);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.hkv * a.num_splits),
@@ -691,7 +704,7 @@ static cudaError_t launch_t(const AttnArgs& a, int row_tiles, cudaStream_t strea
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_e2m1_kernel<D, NT>, a);
+  return cudaLaunchKernelEx(&cfg, decode_e2m1_kernel<D, NT, W>, a);
 }
 
 // Rows per tile: 8 where that holds a request's rows, else 16 (a tile's cached rows
@@ -705,21 +718,40 @@ int decode_e2m1_rows_per_tile(int group, int max_query_len, bool long_rows) {
   return group * (q < 1 ? 1 : q) <= 8 ? 8 : 16;
 }
 
+// Warps per CTA: 8-row tiles run two CTAs of 6 on an SM, or one of 8 where the
+// grid does not give every SM a second one; 16-row tiles (up to 232 registers a
+// thread) one of 8.  A warp alone takes about 2000 cycles a pair of blocks, so
+// what a lone CTA's warps share out counts, against the merge of more warps: one
+// request over 8 KV heads takes, with 6 / 8 / 12 warps, 6.3 / 6.2 / 6.7 us for 512
+// keys (1 split), 7.9 / 7.5 / 7.8 for 4096 (16) and 19.8 / 15.9 / 16.6 for 32768
+// (19).  12 warps in two CTAs an SM are as fast as 16 (the long cases are bound
+// by HBM), and three CTAs of 4 slower.
+constexpr int kWarps8 = 6, kWarps8Lone = 8, kWarps16 = 8;
+
 // Resident CTAs per SM for that tile height.
 int decode_e2m1_ctas_per_sm(int rows_per_tile) {
-  return rows_per_tile == 8 ? Cfg<128, 1>::kCtas : Cfg<128, 2>::kCtas;
+  return rows_per_tile == 8 ? Cfg<128, 1, kWarps8>::kCtas : Cfg<128, 2, kWarps16>::kCtas;
 }
 
-cudaError_t launch_decode_e2m1(const AttnArgs& a, int head_dim, cudaStream_t stream) {
+template <int D>
+static cudaError_t launch_d(const AttnArgs& a, int rows_per_tile, int row_tiles, int num_sms,
+                            cudaStream_t stream) {
+  if (rows_per_tile != 8) return launch_t<D, 2, kWarps16>(a, row_tiles, stream);
+  const int64_t ctas = static_cast<int64_t>(a.hkv) * a.num_splits * row_tiles * a.num_seqs;
+  return ctas <= num_sms ? launch_t<D, 1, kWarps8Lone>(a, row_tiles, stream)
+                         : launch_t<D, 1, kWarps8>(a, row_tiles, stream);
+}
+
+cudaError_t launch_decode_e2m1(const AttnArgs& a, int head_dim, int num_sms,
+                               cudaStream_t stream) {
   const int R = decode_e2m1_rows_per_tile(a.group, a.max_query_len, a.long_rows != 0);
   const int64_t q = a.long_rows || a.max_query_len < kDecodeMaxQ ? a.max_query_len : kDecodeMaxQ;
   const int64_t row_tiles = (a.group * q + R - 1) / R;
   if (row_tiles < 1 || row_tiles > 65535 || a.num_seqs > 65535)
     return cudaErrorInvalidConfiguration;
   const int tiles = static_cast<int>(row_tiles);
-  if (head_dim == 128)
-    return R == 8 ? launch_t<128, 1>(a, tiles, stream) : launch_t<128, 2>(a, tiles, stream);
-  return R == 8 ? launch_t<64, 1>(a, tiles, stream) : launch_t<64, 2>(a, tiles, stream);
+  return head_dim == 128 ? launch_d<128>(a, R, tiles, num_sms, stream)
+                         : launch_d<64>(a, R, tiles, num_sms, stream);
 }
 
 }  // namespace pkv

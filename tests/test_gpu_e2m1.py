@@ -572,3 +572,24 @@ def test_bindings_refuse_wrong_tensors():
             pkv.pkv_write_e2m1(k, v, sl, t["k"], t["v"], 1.0, 1.0)
         with pytest.raises((ValueError, TypeError)):
             pkv.pkv_read_e2m1(t["k"], t["v"], sl, k, v, 1.0, 1.0)
+
+
+def test_the_split_rule_on_this_device():
+    """The rule of the header on this device's SM count, and a workspace sized by it
+    suffices for the library's own choice."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    for seqs, q, length, hq, hkv in [(1, 1, 8192, 32, 8), (1, 1, 1024, 32, 8), (1, 1, 500, 32, 8),
+                                     (2, 1, 131072, 32, 8), (16, 3, 1027, 16, 1), (64, 1, 4096, 32, 8),
+                                     (1, 900, 5000, 32, 8), (1, 1, 65536, 16, 1)]:
+        group = hq // hkv
+        tokens = q if q <= 4 else 1
+        rows = 8 if group * tokens <= 8 else 16
+        units = seqs * hkv * -(-group * tokens // rows)
+        blocks = -(-length // 16)
+        s = max(1, min(blocks // 8, sms * 7 // 8 // units))
+        if blocks > 64 * s:
+            s = min(sms * (2 if rows == 8 else 1) // units, max(s, blocks // 32))
+        s = min(s, 64)
+        if s < 2 or blocks * (s - 1) < 48 * s:
+            s = 1
+        assert pkv.pkv_num_splits_e2m1(seqs, q, length, hq, hkv, 128) == s
