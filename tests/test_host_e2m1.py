@@ -58,6 +58,8 @@ def attend(write=False, **over):
     (dict(seqs=65536, tokens=65536), UNSUPPORTED), (dict(blocks=1 << 27), UNSUPPORTED),
     (dict(splits=2), WORKSPACE), (dict(splits=2, ws=P, ws_bytes=100), WORKSPACE),
     (dict(splits=2, ws=P + 16, ws_bytes=1 << 30), WORKSPACE),
+    (dict(hq=65536, hkv=65536), UNSUPPORTED),
+    (dict(window=64, mq=600000, tokens=600000, width=50000, ms=700000, hq=1, hkv=1), UNSUPPORTED),
     (dict(seqs=0), 0), (dict(tokens=0), 0)])
 def test_attention_calls(write, over, status):
     assert attend(write, **over) == status
