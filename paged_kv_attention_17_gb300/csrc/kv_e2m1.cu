@@ -10,10 +10,19 @@
 //   code = E2M1(RN32(y / s))         (nearest even, at most 6; 0 if s = 0).
 // a / 6 puts the block's largest element on the largest code, up to s's
 // rounding.  A block holding a NaN gets the NaN scale, so the NaN is not lost.
-// Bytes per token: 2 tensors x H x D x (input size + 9 / 16).
+// Bytes per token: 2 tensors x H x D x (input size + 9 / 16).  A thread takes a
+// block of one tensor, the next one's inputs loaded ahead.  8192 tokens of 8 heads
+// of 128 in bf16 take 11.8 us (43.1 MB, 3.65 TB/s, 54% of the measured copy
+// rate): bound by issue (59% busy, 250 instructions a block: nine packed fp32
+// operations a pair of elements for the two quotients), not by HBM.  With plain
+// divisions it took 18.7 us, with the quotients one at a time 12.8.
 //
 // Read.  The inverse: RN32(t * (s * code)), s * code exact, then rounded to the
-// output type.  Bytes per row: 2 tensors x H x D x (9 / 16 + output size).
+// output type.  Bytes per row: 2 tensors x H x D x (9 / 16 + output size).  A
+// thread takes 16 bytes of output of both tensors, striding over the rows: 64
+// contexts (144 thousand rows) of 8 heads of 128 to bf16 take 118.8 us (734 MB,
+// 6.17 TB/s, 91% of the measured copy rate), bound by HBM; a thread per 16 bytes
+// of one tensor without the stride took 211 us.
 #include "e2m1.cuh"
 
 namespace pkv {
