@@ -156,7 +156,7 @@ __device__ __forceinline__ TileRange tile_range(const AttnArgs& a, int q0, int q
   const int n = q1 - q0;
   if (n == 0) return t;
   if (n < 0 || q0 < 0 || q1 > a.num_tokens || n > L || n > a.max_query_len ||
-      (L + kBlock - 1) / kBlock > a.max_blocks_per_seq) {
+      L > static_cast<int64_t>(a.max_blocks_per_seq) * kBlock) {
     t.state = TileRange::kBad;
     return t;
   }

@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(threads_for(KV != kKvBf16), 1)
   const int i_hi = min(i0 + (pairs ? 2 : 1) * kQRows, n) - 1;
   const int kv_len = a.causal ? (L - n + i_hi + 1) : L;
   const int nblk_ctx = (kv_len + kBlock - 1) / kBlock;
-  if ((L + kBlock - 1) / kBlock > a.max_blocks_per_seq) {
+  if (L > static_cast<int64_t>(a.max_blocks_per_seq) * kBlock) {
     if (threadIdx.x == 0) raise_flag(a.flag, PKV_FLAG_BAD_LENGTHS);
     if (a.defer_wait) pdl_wait_primary();
     return;

@@ -260,6 +260,15 @@ def test_windows(window, lens, d):
     b.check(out, lse)
 
 
+@pytest.mark.parametrize("window, causal, splits", [(100, True, 3), (20, False, 1), (200, False, 2),
+                                                    (150, True, 4)])
+def test_windows_with_splits_and_without_a_causal_limit(window, causal, splits):
+    b = Batch(LONG + [(600, 1)], 8, 2, 128, seed=23, window=window, causal=causal)
+    out, lse, flag = b.attend(splits=splits)
+    assert flag.item() == 0
+    b.check(out, lse)
+
+
 @pytest.mark.parametrize("qscale", [0.0, 2.0 ** -60, 2.0 ** -8, 30.0])
 @pytest.mark.parametrize("lens", [DECODE, LONG])
 def test_query_magnitudes(qscale, lens):
@@ -333,6 +342,17 @@ def test_bad_lengths_and_blocks_are_flagged():
     assert flag.item() == pkv.FLAG_BAD_LENGTHS
     t = b.dev()
     t["lens"][0] = 16 * b.width + 1                        # past its table row
+    assert b.attend(t)[2].item() & pkv.FLAG_BAD_LENGTHS
+    t = b.dev()
+    t["lens"][0] = 2 ** 31 - 1                             # and at the type's end
+    assert b.attend(t)[2].item() & pkv.FLAG_BAD_LENGTHS
+    long = Batch([(40, 30)], 4, 2, 128, seed=13)
+    t = long.dev()
+    for length in (2 ** 31 - 1, 16 * long.width + 1, 29, -5):
+        t["lens"][0] = length
+        assert long.attend(t)[2].item() & pkv.FLAG_BAD_LENGTHS
+    t = b.dev()
+    t["qsl"][1] = 5                                        # not nondecreasing, and past the tokens
     assert b.attend(t)[2].item() & pkv.FLAG_BAD_LENGTHS
     for bad in (-1, b.k.shape[0]):
         t = b.dev()
