@@ -313,10 +313,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, W>::kThreads, (Cfg<D, NT, W>::kCtas
     } else if (slot >= 0) {                              // (negative: padding)
       uint2 codes;
       uint32_t scale;
-      float x[16];
-      raw.floats(x);
       const float t = new_v ? a.wv_scale : a.wk_scale;
-      quantise16(x, {t, __fdiv_rn(1.f, t)}, codes, scale);
+      quantise16(raw, {t, __fdiv_rn(1.f, t)}, codes, scale);
       const int row = static_cast<int>(slot % kBlock);
       uint8_t* page = static_cast<uint8_t*>(const_cast<void*>(new_v ? a.v_cache : a.k_cache)) +
                       ((slot / kBlock) * a.hkv + kvh) * P::kBytes;

@@ -72,8 +72,9 @@ struct Divisor {
 __device__ __forceinline__ float quotient_step(float q, float x, float t, float inv) {
   return fmaf(-fmaf(q, t, -x), inv, q);
 }
-// The same on two quotients at once, from nx = -x and ninv = -inv: q0 = nx ninv,
-// then q + (q t + nx) ninv.
+// The same on two quotients (-x) / t at once: from q0 = x ninv, ninv = -inv, each
+// step is q + (q t + x) ninv.  (Negated, so that no operand is: a second division
+// of the negative quotient has the sign of x again.)
 typedef unsigned long long Pair;
 __device__ __forceinline__ Pair pair_of(float lo, float hi) {
   Pair r;
@@ -95,8 +96,8 @@ __device__ __forceinline__ Pair pair_fma(Pair a, Pair b, Pair c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
-__device__ __forceinline__ Pair quotient_step(Pair q, Pair nx, Pair t, Pair ninv) {
-  return pair_fma(pair_fma(q, t, nx), ninv, q);
+__device__ __forceinline__ Pair quotient_step(Pair q, Pair x, Pair t, Pair ninv) {
+  return pair_fma(pair_fma(q, t, x), ninv, q);
 }
 // max(a, |b|, |c|), NaN if any is
 __device__ __forceinline__ float max_abs_nan(float a, float b, float c) {
@@ -129,6 +130,18 @@ struct Raw16 {
       }
     }
   }
+  // The largest magnitude (an infinity or a NaN counts as the larger, by its bits).
+  __device__ __forceinline__ float largest() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(S)); ++i) {
+      const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        m = sizeof(S) == 4 ? max(m, v[k] & 0x7FFFFFFFu) : __vmaxu2(m, v[k] & 0x7FFF7FFFu);
+    }
+    return __uint_as_float(sizeof(S) == 4 ? m : max(m << 16, m & 0xFFFF0000u));
+  }
 };
 
 // (a, b) -> two E2M1 codes, a in the low nibble
@@ -137,6 +150,18 @@ __device__ __forceinline__ uint32_t float2_to_e2m1x2(float a, float b) {
   asm("{\n\t.reg .b8 c;\n\tcvt.rn.satfinite.e2m1x2.f32 c, %1, %2;\n\tcvt.u32.u8 %0, c;\n\t}"
       : "=r"(r)
       : "f"(b), "f"(a));
+  return r;
+}
+
+// Eight values -> eight codes, the first in the low nibble.
+__device__ __forceinline__ uint32_t floats_to_e2m1x8(float2 a, float2 b, float2 c, float2 d) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 c0, c1, c2, c3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c0, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 c1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c2, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 c3, %8, %7;\n\t"
+      "mov.b32 %0, {c0, c1, c2, c3};\n\t}"
+      : "=r"(r)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y), "f"(d.x), "f"(d.y));
   return r;
 }
 
@@ -157,19 +182,14 @@ static __device__ __noinline__ uint3 quantise16_plain(const float* x, float t) {
   return make_uint3(c[0], c[1], scale);
 }
 
-__device__ __forceinline__ void quantise16(const float (&x)[16], const Divisor& d, uint2& codes,
+template <typename S>
+__device__ __forceinline__ void quantise16(const Raw16<S>& raw, const Divisor& d, uint2& codes,
                                            uint32_t& scale) {
-  const Pair t2 = pair_of(d.t, d.t), ninv2 = pair_of(-d.inv, -d.inv), minus = pair_of(-1.f, -1.f);
-  Pair y[8];
-  float a = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const Pair nx = pair_of(-x[2 * i], -x[2 * i + 1]);
-    y[i] = quotient_step(pair_mul(nx, ninv2), nx, t2, ninv2);
-    y[i] = quotient_step(y[i], nx, t2, ninv2);
-    const float2 v = halves(y[i]);
-    a = max_abs_nan(a, v.x, v.y);
-  }
+  float x[16];
+  raw.floats(x);
+  // max |RN(x / t)| = RN(max |x| / t): rounding is monotonic
+  const float top = raw.largest();
+  const float a = quotient_step(quotient_step(top * d.inv, top, d.t, d.inv), top, d.t, d.inv);
   if (!(a <= 1e30f) || !(d.t >= 0x1p-40f && d.t <= 0x1p40f)) {
     float copy[16];
 #pragma unroll
@@ -190,16 +210,18 @@ __device__ __forceinline__ void quantise16(const float (&x)[16], const Divisor& 
   const float s = e4m3x2_to_float2(scale).x;
   float inv;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  const Pair t2 = pair_of(d.t, d.t), ninv2 = pair_of(-d.inv, -d.inv);
   const Pair s2 = pair_of(s, s), nis2 = pair_of(-inv, -inv);
-  uint32_t c[8];
+  float2 z[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const Pair ny = pair_mul(y[i], minus);
-    const float2 z = halves(quotient_step(pair_mul(ny, nis2), ny, s2, nis2));
-    c[i] = float2_to_e2m1x2(z.x, z.y);
+    const Pair x2 = pair_of(x[2 * i], x[2 * i + 1]);
+    Pair y = quotient_step(pair_mul(x2, ninv2), x2, t2, ninv2);   // -y, in the end
+    y = quotient_step(y, x2, t2, ninv2);
+    z[i] = halves(quotient_step(pair_mul(y, nis2), y, s2, nis2));
   }
-  codes = make_uint2(c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24),
-                     c[4] | (c[5] << 8) | (c[6] << 16) | (c[7] << 24));
+  codes = make_uint2(floats_to_e2m1x8(z[0], z[1], z[2], z[3]),
+                     floats_to_e2m1x8(z[4], z[5], z[6], z[7]));
 }
 
 }  // namespace pkv

@@ -50,8 +50,7 @@ __global__ void __launch_bounds__(256, sizeof(S) == 2 ? 4 : 3) kv_write_e2m1_ker
   };
   if (i < 2 * units) fetch(i);
   for (; i < 2 * units; i += stride) {
-    float x[16];
-    raw.floats(x);
+    const Raw16<S> now = raw;
     const int64_t to = slot;
     if (i + stride < 2 * units) fetch(i + stride);
     const bool is_v = i >= units;
@@ -65,7 +64,7 @@ __global__ void __launch_bounds__(256, sizeof(S) == 2 ? 4 : 3) kv_write_e2m1_ker
     }
     uint2 codes;
     uint32_t scale;
-    quantise16(x, is_v ? v_scale : k_scale, codes, scale);
+    quantise16(now, is_v ? v_scale : k_scale, codes, scale);
     const int row = static_cast<int>(to % kBlock);
     uint8_t* page = (is_v ? v_cache : k_cache) + ((to / kBlock) * hkv + h) * P::kBytes;
     *reinterpret_cast<uint2*>(page + row * P::kRowCodes + b * (kQuant / 2)) = codes;
