@@ -13,9 +13,10 @@
 // Bytes per token: 2 tensors x H x D x (input size + 9 / 16).  A thread takes a
 // block of one tensor, the next one's inputs loaded ahead.  8192 tokens of 8 heads
 // of 128 in bf16 take 11.8 us (43.1 MB, 3.65 TB/s, 54% of the measured copy
-// rate): bound by issue (59% busy, 250 instructions a block: nine packed fp32
-// operations a pair of elements for the two quotients), not by HBM.  With plain
-// divisions it took 18.7 us, with the quotients one at a time 12.8.
+// rate); the same loads and stores without the quantising take 8.8, so latency
+// and the arithmetic (eight packed fp32 operations a pair of elements for the two
+// quotients) bound it, not HBM.  With plain divisions it took 18.7 us, with the
+// quotients one at a time 12.8.
 //
 // Read.  The inverse: RN32(t * (s * code)), s * code exact, then rounded to the
 // output type.  Bytes per row: 2 tensors x H x D x (9 / 16 + output size).  A
