@@ -228,9 +228,11 @@ int pkv_num_splits(int num_seqs, int max_query_len, int max_seq_len, int num_q_h
 
 /*
  * pkv_num_splits_e2m1 - the same for pkv_attention_varlen_e2m1, whose tiles hold
- * 8 or 16 rows and whose CTAs run one or two to an SM: U units as above (one
- * decode token a request where max_query_len > PKV_DECODE_MAX_QLEN), B blocks of
- * max_seq_len, s = min(B / 8, 7/8 SMs / U); where that leaves a split more than 64
+ * 8 rows (two CTAs fit an SM) or 16 (one).  A request has G query heads to a KV
+ * head x max_query_len rows (1 token where max_query_len > PKV_DECODE_MAX_QLEN),
+ * B blocks of max_seq_len; tiles of 16 rows are taken where it has more than 8 and
+ * num_seqs x num_kv_heads x its tiles x max(1, B / 32) exceeds the SMs.  With U
+ * units as above, s = min(B / 8, 7/8 SMs / U); where that leaves a split more than 64
  * blocks, s = min(CTA slots / U, max(s, B / 32)); at most 64, and 1 where the
  * split would not save B (s - 1) / s >= 48 blocks.  Returns 0 for invalid
  * arguments or device.
@@ -435,7 +437,11 @@ pkv_status pkv_write_attention_varlen_e4m3(
  * are widened exactly to f16; each q row enters as f16 scaled by a power of two
  * (its largest magnitude in [2^14, 2^15): exact for every element within 2^31
  * of it); both contractions run on tensor cores with fp32 accumulation, P
- * rounded to f16 for P.V.
+ * rounded to f16 for P.V.  Requests with n > PKV_DECODE_MAX_QLEN take the
+ * tcgen05 prefill tiles (pages widened in shared memory) at a positive
+ * softmax_scale without a window below 128 keys, else the decode kernel's 16-row
+ * tiles; PKV_ERR_UNSUPPORTED for more than 65535 KV heads, or on those tiles for
+ * more than 524280 rows (query heads of a KV head x max_query_len) a request.
  *   q, out            device bf16 [num_tokens, num_q_heads, head_dim].
  *   k_cache, v_cache  device, [num_blocks, num_kv_heads, 9 * head_dim] bytes.
  *   k_scale, v_scale  finite, > 0 (else PKV_ERR_INVALID_ARG).

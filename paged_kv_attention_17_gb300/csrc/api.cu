@@ -30,7 +30,8 @@ cudaError_t launch_kv_read_e2m1(const void* k_cache, const void* v_cache, const 
                                 int64_t num_slots, int hkv, int head_dim, float k_scale,
                                 float v_scale, int32_t* flag, int num_sms, cudaStream_t stream);
 cudaError_t launch_decode_e2m1(const AttnArgs& a, int head_dim, int num_sms, cudaStream_t stream);
-int decode_e2m1_rows_per_tile(int group, int max_query_len, bool long_rows);
+int decode_e2m1_rows_per_tile(int group, int max_query_len, bool long_rows, int64_t seq_heads,
+                              int64_t nblk, int num_sms);
 int decode_e2m1_ctas_per_sm(int rows_per_tile);
 cudaError_t launch_decode(const AttnArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
                           ElemType et, int head_dim, bool pdl, cudaStream_t stream);
@@ -215,7 +216,10 @@ int split_rule(int num_seqs, int max_query_len, int max_seq_len, int num_q_heads
   const bool e2m1 = et == ElemType::kE2m1;
   const int qmax = max_query_len < 1 ? 1 : max_query_len;
   const int qd = qmax <= kDecodeMaxQ ? qmax : (e2m1 ? 1 : kDecodeMaxQ);
-  const int R = e2m1 ? decode_e2m1_rows_per_tile(group, qmax, false)
+  const int64_t nblk = (static_cast<int64_t>(max_seq_len) + kBlock - 1) / kBlock;
+  const int R = e2m1 ? decode_e2m1_rows_per_tile(group, qmax, false,
+                                                 static_cast<int64_t>(num_seqs) * num_kv_heads,
+                                                 nblk, sms)
                      : decode_rows_per_tile(group, qd, false);
   const int64_t units = static_cast<int64_t>(num_seqs) * num_kv_heads * ((group * qd + R - 1) / R);
   // decode CTA slots of the device (two per SM for the tensor-core build);
@@ -225,7 +229,6 @@ int split_rule(int num_seqs, int max_query_len, int max_seq_len, int num_q_heads
   const int64_t capacity =
       static_cast<int64_t>(sms) *
       (e2m1 ? decode_e2m1_ctas_per_sm(R) : decode_ctas_per_sm(et, head_dim));
-  const int64_t nblk = (static_cast<int64_t>(max_seq_len) + kBlock - 1) / kBlock;
   if (e2m1) return split_rule_e2m1(units, nblk, sms, capacity);
   const int64_t target = capacity * 7 / 8;
   int64_t s = target / units;

@@ -190,7 +190,8 @@ PyObject* attention(PyObject* const* a, Py_ssize_t n) {
   if (!as_int(c.heads) || !as_int(c.dim) || !as_int(hq) || !as_int(seqs) || !as_int(width) ||
       !as_int(mq) || !as_int(ms) || !as_int(splits) || !as_int(window))
     return PyErr_Format(PyExc_ValueError, "a size or count does not fit 32 bits");
-  const int causal = PyObject_IsTrue(a[16]) ? 1 : 0;
+  const int causal = PyObject_IsTrue(a[16]);
+  if (causal < 0) return nullptr;
   auto i = [](int64_t v) { return static_cast<int>(v); };
   int status;
   if (a[1] == Py_None) {

@@ -75,7 +75,7 @@ struct AttnArgs {
   // instead of two query heads of one tile (see prefill.cu).
   int pair_tiles;
   // Unsplit decode launch of 2..256 requests: blockIdx.z is read as a rank of
-  // the requests by decreasing seq_len (longest first; see decode.cu).
+  // the requests by decreasing seq_len (request_by_length_rank below).
   int lpt;
   const void* k_new;      // [num_tokens, hkv, D], the cache's element type
   const void* v_new;

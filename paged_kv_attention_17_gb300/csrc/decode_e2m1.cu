@@ -715,15 +715,26 @@ static cudaError_t launch_t(const AttnArgs& a, int row_tiles, cudaStream_t strea
   return cudaLaunchKernelEx(&cfg, decode_e2m1_kernel<D, NT, W>, a);
 }
 
-// Rows per tile: 8 where that holds a request's rows, else 16 (a tile's cached rows
-// are read once for all of its rows).  Beside requests that the prefill kernel
-// takes (max_query_len above the decode bound, no long_rows), the decode rows
-// are taken to be single tokens, as such batches have them.
-int decode_e2m1_rows_per_tile(int group, int max_query_len, bool long_rows) {
+// Rows per tile.  8 where that holds a request's rows; else 16, whose tiles read
+// the cached rows once for all of them, unless the batch (seq_heads requests x KV
+// heads, of nblk blocks) is too small for its 16-row tiles to fill the SMs at 32
+// blocks a CTA: then 8-row tiles share out the latency.  Measured, us, 16 / 8
+// rows: 16 requests of 3 tokens, 16 query heads to one KV head, 1027 keys 13.0 /
+// 10.3; one request of 8192 keys, so headed, 9.2 / 7.5; 16 requests of 4 tokens,
+// 32 / 8 heads, 2048 keys 19.7 / 21.5; 64 requests, 32 / 2 heads, 4096 keys 30.9 /
+// 35.7.  Beside requests that the prefill kernel takes (max_query_len above the
+// decode bound, no long_rows), the decode rows are taken to be single tokens, as
+// such batches have them.
+int decode_e2m1_rows_per_tile(int group, int max_query_len, bool long_rows, int64_t seq_heads,
+                              int64_t nblk, int num_sms) {
   const int64_t q = long_rows                     ? max_query_len
                     : max_query_len > kDecodeMaxQ ? 1
                                                   : max_query_len;
-  return group * (q < 1 ? 1 : q) <= 8 ? 8 : 16;
+  const int64_t rows = group * (q < 1 ? 1 : q);
+  if (rows <= 8) return 8;
+  if (long_rows) return 16;
+  const int64_t ctas = seq_heads * ((rows + 15) / 16) * (nblk < 32 ? 1 : nblk / 32);
+  return ctas <= num_sms ? 8 : 16;
 }
 
 // Warps per CTA: 8-row tiles run two CTAs of 6 on an SM, or one of 8 where the
@@ -752,7 +763,11 @@ static cudaError_t launch_d(const AttnArgs& a, int rows_per_tile, int row_tiles,
 
 cudaError_t launch_decode_e2m1(const AttnArgs& a, int head_dim, int num_sms,
                                cudaStream_t stream) {
-  const int R = decode_e2m1_rows_per_tile(a.group, a.max_query_len, a.long_rows != 0);
+  const int span = a.window > 0 && a.window < a.max_seq_len - kDecodeMaxQ
+                       ? a.window + kDecodeMaxQ : a.max_seq_len;
+  const int R = decode_e2m1_rows_per_tile(a.group, a.max_query_len, a.long_rows != 0,
+                                          static_cast<int64_t>(a.num_seqs) * a.hkv,
+                                          (static_cast<int64_t>(span) + kBlock - 1) / kBlock, num_sms);
   const int64_t q = a.long_rows || a.max_query_len < kDecodeMaxQ ? a.max_query_len : kDecodeMaxQ;
   const int64_t row_tiles = (a.group * q + R - 1) / R;
   if (row_tiles < 1 || row_tiles > 65535 || a.num_seqs > 65535)

@@ -228,6 +228,16 @@ def test_decode_rows(hq, hkv, d, splits):
     b.check(out, lse)
 
 
+@pytest.mark.parametrize("splits", [0, 1, 2])
+@pytest.mark.parametrize("hq, hkv, d", [(64, 4, 128), (64, 4, 64)])
+def test_sixteen_row_tiles(hq, hkv, d, splits):
+    # (batches that fill the device with 16-row tiles)
+    b = Batch([(200 + 17 * r, 1 + r % 4) for r in range(24)], hq, hkv, d, seed=24)
+    out, lse, flag = b.attend(splits=splits)
+    assert flag.item() == 0
+    b.check(out, lse)
+
+
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("lens", [[(4, 4), (20, 2), (35, 3), (5, 1)], [(900, 4), (0, 0), (129, 3)]])
 @pytest.mark.parametrize("hq, hkv, d", [(8, 4, 64), (8, 2, 128), (16, 1, 128)])
@@ -600,12 +610,14 @@ def test_the_split_rule_on_this_device():
     sms = torch.cuda.get_device_properties(0).multi_processor_count
     for seqs, q, length, hq, hkv in [(1, 1, 8192, 32, 8), (1, 1, 1024, 32, 8), (1, 1, 500, 32, 8),
                                      (2, 1, 131072, 32, 8), (16, 3, 1027, 16, 1), (64, 1, 4096, 32, 8),
-                                     (1, 900, 5000, 32, 8), (1, 1, 65536, 16, 1)]:
+                                     (1, 900, 5000, 32, 8), (1, 1, 65536, 16, 1),
+                                     (64, 4, 4000, 32, 8), (2, 2, 300, 128, 8)]:
         group = hq // hkv
         tokens = q if q <= 4 else 1
-        rows = 8 if group * tokens <= 8 else 16
-        units = seqs * hkv * -(-group * tokens // rows)
         blocks = -(-length // 16)
+        full = seqs * hkv * -(-group * tokens // 16) * max(1, blocks // 32) > sms
+        rows = 16 if group * tokens > 8 and full else 8
+        units = seqs * hkv * -(-group * tokens // rows)
         s = max(1, min(blocks // 8, sms * 7 // 8 // units))
         if blocks > 64 * s:
             s = min(sms * (2 if rows == 8 else 1) // units, max(s, blocks // 32))
