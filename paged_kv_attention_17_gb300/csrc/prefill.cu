@@ -56,11 +56,19 @@
 // largest p.  A NaN scale of V in a tile that crosses a mask edge is widened to
 // zeros and noted: the rows that see its key take the NaN at the end, the rows
 // that do not are untouched (0 * NaN would reach them through the MMA).  Interior
-// tiles take a branch-free widening (8192 causal tokens, 32 / 8 heads of 128: 490
-// us, 1121 TFLOP/s; with the edge tests in every unit 813).  Without the widening's
-// conversions it would take 464 us, without exponentials 481, without nearly all
-// MMAs 422: the chain of a tile's two softmax passes bounds it, as it bounds the
-// other caches' tiles.
+// tiles take a branch-free widening (8192 causal tokens, 32 / 8 heads of 128: 453
+// us, 1213 TFLOP/s; bf16 427 us, E4M3 466).
+//
+// What bounds a key tile (about 4000 cycles for both heads, 2048 of them MMAs), by
+// the clock read at each role's steps: one head's chain of scores to registers 130,
+// maximum 300-600, exponentials 700-1050, P converted and stored 400, then 250
+// until the issuer sees the last arrival, and 1500 from P.V's issue to the next
+// scores; the upper figures are those of the warps that share a sub-partition
+// with a widening warp.  The other head's chain fills its gaps.  So whatever is
+// off that chain is done before it: the issuer waits for K and V before it waits
+// for P, and P.V's completion is not waited for by itself (489 -> 453 us).  Four
+// widening warps, one to a sub-partition, cost more in shared-memory traffic
+// beside the S MMAs than they save (496).
 #include <algorithm>
 
 #include "common.cuh"
@@ -645,7 +653,7 @@ __global__ void __launch_bounds__(threads_for(KV != kKvBf16), 1)
         for (int k = 0; k < 8; ++k)
           umma_ts(tbase + 2 * kKeys + t * 128, tbase + t * kKeys + k * 8,
                   b0 + static_cast<uint64_t>((k * 2048) >> 4), id_o, (kt > 0 || k > 0) ? 1u : 0u);
-        umma_commit(&bar_o[t]);
+        if (kt == ntk - 1) umma_commit(&bar_o[t]);
       };
       auto wait_k = [&](int kt) {
         if (!mbar_wait(&k_full[kt % kStages], (kt / kStages) & 1)) return false;
@@ -665,13 +673,14 @@ __global__ void __launch_bounds__(threads_for(KV != kKvBf16), 1)
       }
       for (int kt = 0; ok && kt < ntk; ++kt) {
         const bool more = kt + 1 < ntk;
-        if (!mbar_wait(&bar_p[0], kt & 1) || !wait_v(kt)) { ok = false; break; }
+        // the operands first: they have usually landed by the time P has
+        if (!wait_v(kt) || (more && !wait_k(kt + 1)) || !mbar_wait(&bar_p[0], kt & 1)) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
         issue_pv(0, kt);
-        if (more) {
-          if (!wait_k(kt + 1)) { ok = false; break; }
-          issue_s(0, kt + 1);
-        }
+        if (more) issue_s(0, kt + 1);
         if (!mbar_wait(&bar_p[1], kt & 1)) { ok = false; break; }
         tc_fence_after();
         issue_pv(1, kt);
@@ -963,13 +972,8 @@ __global__ void __launch_bounds__(threads_for(KV != kKvBf16), 1)
         tmem_st32u(t_s + 32 * c, w);
       }
       if (kt > 0) {
-        // the previous P.V of this tile must be done before O is rescaled
-        const bool got_o = mbar_wait(&bar_o[t], (kt - 1) & 1);
-        if (!__all_sync(0xffffffffu, got_o)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
+        // (the previous P.V of this tile is done: it was issued before these
+        // scores' MMAs, and their commit covers it)
         if (__any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll
           for (int c = 0; c < kOC; ++c) {
@@ -1005,7 +1009,7 @@ __global__ void __launch_bounds__(threads_for(KV != kKvBf16), 1)
       mbar_arrive(&bar_p[t]);
     }
     // ---- epilogue: O row / l -> output dtype, lse ----
-    bool got_o = ok && mbar_wait(&bar_o[t], (ntk - 1) & 1);
+    bool got_o = ok && mbar_wait(&bar_o[t], 0);
     got_o = __all_sync(0xffffffffu, got_o);
     if (!got_o) {
       ok = false;
