@@ -534,6 +534,34 @@ def test_captured_and_replayed_on_another_stream(lens):
     assert flag.item() == 0
 
 
+@pytest.mark.parametrize("lens", [[(300, 1), (47, 1)], [(290, 130), (200, 1)]])
+def test_a_stream_given_by_argument(lens):
+    """Two streams at once, neither of them current, a workspace and rows of their own."""
+    b = Batch(lens, 8, 2, 128, seed=20)
+    t = b.dev()
+    want, lse_want, _ = b.attend(t)
+    n = want.shape[0]
+    slots = torch.from_numpy(np.concatenate([b.slot_range(r, L - k, L) for r, (L, k) in enumerate(lens)])).to(DEV)
+    read = [torch.empty(n, 2, 128, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    pkv.pkv_read_e2m1(t["k"], t["v"], slots, read[0], read[1], b.ks, b.vs)
+    runs = []
+    for _ in range(2):
+        runs.append((torch.cuda.Stream(), torch.empty_like(want), torch.empty_like(lse_want),
+                     torch.empty(8 << 20, dtype=torch.uint8, device=DEV),
+                     torch.zeros(1, dtype=torch.int32, device=DEV), [torch.empty_like(x) for x in read]))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for side, out, lse, ws, flag, rows in runs:
+            pkv.pkv_attention_varlen_e2m1(t["q"], t["k"], t["v"], out, t["qsl"], t["lens"], t["table"], b.mq,
+                                          b.ms, b.scale, b.ks, b.vs, workspace=ws, lse_out=lse,
+                                          error_flag=flag, stream=side)
+            pkv.pkv_read_e2m1(t["k"], t["v"], slots, rows[0], rows[1], b.ks, b.vs, stream=side)
+    for side, out, lse, _, flag, rows in runs:
+        side.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, lse_want) and flag.item() == 0
+        assert torch.equal(rows[0], read[0]) and torch.equal(rows[1], read[1])
+
+
 @pytest.mark.parametrize("inputs", ["stage", "mapped", "memcpy"])
 @pytest.mark.parametrize("d", [64, 128])
 def test_decode_graph_runner_steps(inputs, d):
