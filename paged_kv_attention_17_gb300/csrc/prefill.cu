@@ -890,7 +890,9 @@ __global__ void __launch_bounds__(threads_for(KV != kKvBf16), 1)
           v.w = bf16x2_to_f16x2_scaled(v.w, down);
           sts128(pc, v);
         }
-        sc *= __int_as_float((127 + e) << 23);
+        // (at least the least normal float: a masked -inf times 0 would be a NaN,
+        // where scores this small are all 0 beside each other anyway)
+        sc = fmaxf(sc * __int_as_float((127 + e) << 23), 1.17549435e-38f);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         mbar_arrive(bar_qr);
       }
