@@ -1841,9 +1841,12 @@ __global__ void __launch_bounds__(128) combine_kernel(const AttnArgs a) {
     const int n = q1 - q0;
     if (n <= 0 || n > kDecodeMaxQ || i >= n || q0 < 0 || q1 > a.num_tokens || n > L) return;
   }
+  // A NaN partial log-sum-exp (E2M1: the split saw a NaN score) gets a NaN weight,
+  // also beside splits without a key, so the row's output and log-sum-exp are NaN
+  // as those of an unsplit row.  The other caches' partials hold no NaN here.
   float M = warp_max(fmaxf(l0, l1));
-  const float w0 = M == -INFINITY ? 0.f : ex2(l0 - M);
-  const float w1 = M == -INFINITY ? 0.f : ex2(l1 - M);
+  const float w0 = l0 == -INFINITY ? 0.f : ex2(l0 - M);
+  const float w1 = l1 == -INFINITY ? 0.f : ex2(l1 - M);
   const float wsum = warp_sum(w0 + w1);
   float o[kDPL];
 #pragma unroll
@@ -1890,7 +1893,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const AttnArgs a) {
     for (int e = 0; e < kDPL; ++e) store_elem<T>(a.out, base + e, v[e]);
   }
   if (a.lse_out != nullptr && lane == 0)
-    a.lse_out[t * a.hq + h] = wsum > 0.f ? (M + lg2(wsum)) * kLn2 : -INFINITY;
+    a.lse_out[t * a.hq + h] = wsum == 0.f ? -INFINITY : (M + lg2(wsum)) * kLn2;
 }
 
 // The shared-prefix merge (cascade pass 3): for each (token, q head) row,
