@@ -154,6 +154,24 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _scratch(nbytes, device, stream):
+    """A workspace that is given up when the call returns, in torch's memory of the
+    call's own stream: what it is handed out for next runs behind the call's
+    kernels, and what it held before ran ahead of them.  (Memory of the current
+    stream would be free for that stream's next tensor while another stream's
+    kernels still use it.)"""
+    current = torch.cuda.current_stream(device)
+    handle = _stream(stream).value or 0
+    if stream is None or handle == current.cuda_stream:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if handle <= 1:                                      # NULL and cudaStreamLegacy
+        stream = torch.cuda.default_stream(device)
+    elif not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(handle, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def _check(func, code):
     if code != PKV_OK:
         raise PkvError(func, code)
@@ -212,17 +230,18 @@ def pkv_workspace_bytes(num_seqs, num_q_heads, head_dim, num_splits) -> int:
                                          int(num_splits)))
 
 
-def _splits_and_workspace(q, hkv, num_seqs, max_query_len, span, num_splits, workspace):
+def _splits_and_workspace(q, hkv, num_seqs, max_query_len, span, num_splits, workspace, stream):
     """The split count (pkv_num_splits for a context of ``span`` keys when
     num_splits is 0) and a workspace for its partials: the caller's, or one
-    allocated with torch here when none is given and one is needed."""
+    allocated with torch here, for the call's stream, when none is given and one
+    is needed."""
     _, hq, d = q.shape
     splits = int(num_splits)
     if splits == 0 and num_seqs > 0:
         splits = pkv_num_splits(num_seqs, max_query_len, span, hq, hkv, d, q.device.index)
     need = pkv_workspace_bytes(num_seqs, hq, d, splits)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _scratch(need, q.device, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     return splits, workspace, ws_bytes
 
@@ -250,7 +269,8 @@ def pkv_attention_varlen(q, k_cache, v_cache, out, query_start_loc, seq_lens, bl
     nb, bs, hkv, _ = k_cache.shape
     num_seqs = int(seq_lens.numel())
     splits, workspace, ws_bytes = _splits_and_workspace(
-        q, hkv, num_seqs, max_query_len, split_span(max_seq_len, window), num_splits, workspace)
+        q, hkv, num_seqs, max_query_len, split_span(max_seq_len, window), num_splits, workspace,
+        stream)
     if window:
         code = lib().pkv_attention_varlen_window(
             _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(lse_out),
@@ -282,7 +302,7 @@ def pkv_write_attention_varlen(k_new, v_new, slot_mapping, q, k_cache, v_cache, 
     nb, bs, hkv, _ = k_cache.shape
     num_seqs = int(seq_lens.numel())
     splits, workspace, ws_bytes = _splits_and_workspace(
-        q, hkv, num_seqs, max_query_len, max_seq_len, num_splits, workspace)
+        q, hkv, num_seqs, max_query_len, max_seq_len, num_splits, workspace, stream)
     code = lib().pkv_write_attention_varlen(
         _ptr(k_new), _ptr(v_new), _ptr(slot_mapping), _ptr(q), _ptr(k_cache), _ptr(v_cache),
         _ptr(out), _ptr(lse_out), _ptr(query_start_loc), _ptr(seq_lens), _ptr(block_table),
@@ -309,7 +329,7 @@ def pkv_write_attention_varlen_e4m3(k_new, v_new, slot_mapping, q, k_cache, v_ca
     nb, bs, hkv, _ = k_cache.shape
     num_seqs = int(seq_lens.numel())
     splits, workspace, ws_bytes = _splits_and_workspace(
-        q, hkv, num_seqs, max_query_len, max_seq_len, num_splits, workspace)
+        q, hkv, num_seqs, max_query_len, max_seq_len, num_splits, workspace, stream)
     code = lib().pkv_write_attention_varlen_e4m3(
         _ptr(k_new), _ptr(v_new), _ptr(slot_mapping), _ptr(q), _ptr(k_cache), _ptr(v_cache),
         _ptr(out), _ptr(lse_out), _ptr(query_start_loc), _ptr(seq_lens), _ptr(block_table),
@@ -337,7 +357,8 @@ def pkv_attention_varlen_e4m3(q, k_cache, v_cache, out, query_start_loc, seq_len
     nb, bs, hkv, _ = k_cache.shape
     num_seqs = int(seq_lens.numel())
     splits, workspace, ws_bytes = _splits_and_workspace(
-        q, hkv, num_seqs, max_query_len, split_span(max_seq_len, window), num_splits, workspace)
+        q, hkv, num_seqs, max_query_len, split_span(max_seq_len, window), num_splits, workspace,
+        stream)
     if window:
         code = lib().pkv_attention_varlen_e4m3_window(
             _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(lse_out),
@@ -419,7 +440,7 @@ def pkv_cascade_attention(q, k_cache, v_cache, out, query_start_loc, suffix_lens
         splits = pkv_cascade_splits(n_tok, shared, hq, hkv, d, rule, q.device.index)
     need = pkv_cascade_workspace_bytes(n_tok, hq, d, splits)
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(max(need, 256), q.device, stream)
     ws_bytes = workspace.numel() * workspace.element_size()
     if e4m3:
         code = lib().pkv_cascade_attention_e4m3(
@@ -525,7 +546,7 @@ def _e2m1_attention(name, k_new, v_new, slots, q, k_cache, v_cache, out, query_s
                                              hq, k_cache.shape[1], d, device)
         nbytes = pkv_workspace_bytes(seqs, hq, d, num_splits)
         if nbytes:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=k_cache.device)
+            workspace = _scratch(nbytes, k_cache.device, stream)
     status = calls.attention(_address[name], k_new, v_new, slots, q, k_cache, v_cache, out,
                              query_start_loc, seq_lens, block_table, max_query_len, max_seq_len,
                              softmax_scale, k_scale, v_scale, causal, num_splits, workspace,
