@@ -547,7 +547,8 @@ def _e2m1_attention(name, k_new, v_new, slots, q, k_cache, v_cache, out, query_s
         nbytes = pkv_workspace_bytes(seqs, hq, d, num_splits)
         if nbytes:
             workspace = _scratch(nbytes, k_cache.device, stream)
-    status = calls.attention(_address[name], k_new, v_new, slots, q, k_cache, v_cache, out,
+    write = name == "pkv_write_attention_varlen_e2m1"
+    status = calls.attention(_address[name], write, k_new, v_new, slots, q, k_cache, v_cache, out,
                              query_start_loc, seq_lens, block_table, max_query_len, max_seq_len,
                              softmax_scale, k_scale, v_scale, causal, num_splits, workspace,
                              lse_out, error_flag, window, device, raw)

@@ -142,17 +142,28 @@ PyObject* rows(PyObject* const* a, Py_ssize_t n) {
   return PyLong_FromLong(status);
 }
 
-// attention(function, k_new, v_new, slots, q, k_cache, v_cache, out, query_start_loc,
-//           seq_lens, block_table, max_query_len, max_seq_len, softmax_scale, k_scale,
-//           v_scale, causal, num_splits, workspace, lse_out, error_flag, window,
-//           device, stream) -> status
-// k_new, v_new and slots are None for the call that writes nothing.
-PyObject* attention(PyObject* const* a, Py_ssize_t n) {
-  if (n != 24) return PyErr_Format(PyExc_TypeError, "attention takes 24 arguments");
+// attention(function, write, k_new, v_new, slots, q, k_cache, v_cache, out,
+//           query_start_loc, seq_lens, block_table, max_query_len, max_seq_len,
+//           softmax_scale, k_scale, v_scale, causal, num_splits, workspace, lse_out,
+//           error_flag, window, device, stream) -> status
+// `write` says which of the two signatures the function has; k_new, v_new and slots
+// are tensors then, and are not looked at otherwise.
+PyObject* attention(PyObject* const* args, Py_ssize_t n) {
+  if (n != 25) return PyErr_Format(PyExc_TypeError, "attention takes 25 arguments");
+  const int write = PyObject_IsTrue(args[1]);
+  if (write < 0) return nullptr;
+  PyObject* const* a = args + 1;                         // (a[1], a[2], a[3]: the new rows)
+  const Tensor *k = nullptr, *v = nullptr, *slots = nullptr;
+  if (write) {
+    k = tensor(a[1], "k_new");
+    v = k ? tensor(a[2], "v_new") : nullptr;
+    slots = v ? tensor(a[3], "slot_mapping") : nullptr;
+    if (slots == nullptr) return nullptr;
+  }
   int64_t fn, device, stream, mq, ms, splits, window;
   float scale, ks, vs;
   Caches c;
-  if (!integer(a[0], &fn) || !integer(a[22], &device) || !integer(a[23], &stream) ||
+  if (!integer(args[0], &fn) || !integer(a[22], &device) || !integer(a[23], &stream) ||
       !integer(a[11], &mq) || !integer(a[12], &ms) || !integer(a[17], &splits) ||
       !integer(a[21], &window) || !number(a[13], &scale) || !number(a[14], &ks) ||
       !number(a[15], &vs) || !caches(a[5], a[6], static_cast<int>(device), &c))
@@ -194,7 +205,7 @@ PyObject* attention(PyObject* const* a, Py_ssize_t n) {
   if (causal < 0) return nullptr;
   auto i = [](int64_t v) { return static_cast<int>(v); };
   int status;
-  if (a[1] == Py_None) {
+  if (!write) {
     using Fn = int (*)(const void*, const void*, const void*, void*, void*, const void*,
                        const void*, const void*, int, int, int64_t, int, int, int, int, int, int,
                        float, float, float, int, int, int, void*, size_t, void*, int64_t, void*);
@@ -204,10 +215,7 @@ PyObject* attention(PyObject* const* a, Py_ssize_t n) {
         16, scale, ks, vs, causal, i(window), i(splits), workspace, workspace_bytes, flag,
         c.blocks, reinterpret_cast<void*>(stream));
   } else {
-    const Tensor* k = tensor(a[1], "k_new");
-    const Tensor* v = k ? tensor(a[2], "v_new") : nullptr;
-    const Tensor* slots = v ? tensor(a[3], "slot_mapping") : nullptr;
-    if (slots == nullptr || !fits(*k, "k_new", at::kBFloat16, c.device, {tokens, c.heads, c.dim}) ||
+    if (!fits(*k, "k_new", at::kBFloat16, c.device, {tokens, c.heads, c.dim}) ||
         !fits(*v, "v_new", at::kBFloat16, c.device, {tokens, c.heads, c.dim}) ||
         !fits(*slots, "slot_mapping", at::kLong, c.device, {tokens}))
       return nullptr;
