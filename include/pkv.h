@@ -440,8 +440,9 @@ pkv_status pkv_write_attention_varlen_e4m3(
  * rounded to f16 for P.V.  Requests with n > PKV_DECODE_MAX_QLEN take the
  * tcgen05 prefill tiles (pages widened in shared memory) at a positive
  * softmax_scale without a window below 128 keys, else the decode kernel's 16-row
- * tiles; PKV_ERR_UNSUPPORTED for more than 65535 KV heads, or on those tiles for
- * more than 524280 rows (query heads of a KV head x max_query_len) a request.
+ * tiles; PKV_ERR_UNSUPPORTED for more than 65535 KV heads, on those tiles for
+ * more than 524280 rows (query heads of a KV head x max_query_len) a request, and
+ * for more than 1048560 decode rows (x min(max_query_len, PKV_DECODE_MAX_QLEN)).
  *   q, out            device bf16 [num_tokens, num_q_heads, head_dim].
  *   k_cache, v_cache  device, [num_blocks, num_kv_heads, 9 * head_dim] bytes.
  *   k_scale, v_scale  finite, > 0 (else PKV_ERR_INVALID_ARG).

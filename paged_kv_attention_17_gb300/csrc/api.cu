@@ -331,11 +331,12 @@ static pkv_status attention(const void* q, const void* k_cache, const void* v_ca
   const bool codes = et == ElemType::kE4m3 || et == ElemType::kE2m1;
   a.long_rows = tc_prefill ? 0 : (codes ? (max_query_len > kDecodeMaxQ) : 1);
   // (E2M1: byte offsets within a block's pages stay in 32 bits, and a request's
-  // row tiles in the grid)
+  // row tiles in the grid; that many decode rows take tiles of 16)
+  const int64_t group = num_q_heads / num_kv_heads;
   if (et == ElemType::kE2m1 &&
       (num_kv_heads > 65535 ||
-       (a.long_rows &&
-        static_cast<int64_t>(num_q_heads / num_kv_heads) * max_query_len > 65535ll * 8)))
+       (a.long_rows ? group * max_query_len > 65535ll * 8
+                    : group * std::min(max_query_len, kDecodeMaxQ) > 65535ll * 16)))
     return PKV_ERR_UNSUPPORTED;
   if (need > 0) {
     const size_t rows = static_cast<size_t>(splits) * num_seqs * kDecodeMaxQ * num_q_heads;
