@@ -2,7 +2,7 @@
 
 Argument marshalling only: each wrapper reads pointers, shapes and the current
 CUDA stream from torch tensors and calls the C entry point of the same name
-(the E2M1 ones through ``_calls.so``, which reads and checks the tensors in
+(the E2M1 ones through ``_lib/_calls.*.so``, which reads and checks the tensors in
 compiled code); every step of the computation runs in the library's CUDA kernels.  There is no
 fallback: if the library is missing or a call fails, an exception is raised.
 """
@@ -16,7 +16,6 @@ import os
 import torch
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "libpkv.so")
-_CALLS_PATH = os.path.join(os.path.dirname(_LIB_PATH), "_calls.so")
 _lib = None
 
 PKV_OK = 0
@@ -472,13 +471,15 @@ def _load_calls():
     """The compiled argument checks (``csrc/calls.cpp``), and the addresses of the
     library functions that they call."""
     global _calls
-    if not os.path.exists(_CALLS_PATH):
-        raise ImportError(f"not built: {_CALLS_PATH} is missing "
+    from .build import calls_path
+    path = calls_path()
+    if not os.path.exists(path):
+        raise ImportError(f"not built: {path} is missing "
                           "(run paged_kv_attention_17_gb300.build.build())")
     for name in ("pkv_write_e2m1", "pkv_read_e2m1", "pkv_attention_varlen_e2m1",
                  "pkv_write_attention_varlen_e2m1"):
         _address[name] = ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value
-    spec = importlib.util.spec_from_file_location("_calls", _CALLS_PATH)
+    spec = importlib.util.spec_from_file_location("_calls", path)
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)
     _calls = module

@@ -2,9 +2,10 @@
 
 Each ``csrc/*.cu`` file is compiled by nvcc in parallel, then linked into one
 shared library with the CUDA runtime linked statically; beside them the host
-compiler builds ``_lib/_calls.so`` (``csrc/calls.cpp``), the Python binding's
-argument checks for the E2M1 calls, against this interpreter and its torch.
-Rebuilds only when a source or header is newer than the library.
+compiler builds ``_lib/_calls.<interpreter>-torch<version>.so``
+(``csrc/calls.cpp``), the Python binding's argument checks for the E2M1 calls,
+against this interpreter and its torch.  Rebuilds the one or the other only when it
+is missing or a source or header of it is newer.
 """
 
 from __future__ import annotations
@@ -22,7 +23,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libpkv.so")
-CALLS = os.path.join(OUT_DIR, "_calls.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", INCLUDE, "-I", CSRC]
@@ -38,19 +38,34 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def calls_path() -> str:
+    """The compiled argument checks for this interpreter and this torch (their ABI
+    is in the name: another one's are never loaded)."""
+    import torch
+    tag = f"{sysconfig.get_config_var('SOABI')}-torch{torch.__version__}"
+    return os.path.join(OUT_DIR, f"_calls.{tag}.so")
+
+
+def _older(built: str, deps) -> bool:
+    return not os.path.exists(built) or any(os.path.getmtime(p) > os.path.getmtime(built)
+                                            for p in deps)
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(CALLS):
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
-    deps = _sources() + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
-    return any(os.path.getmtime(p) > t for p in deps)
+    return _older(LIB, _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) +
+                  glob.glob(os.path.join(INCLUDE, "*.h")))
+
+
+def _calls_stale() -> bool:
+    return _older(calls_path(), [os.path.join(CSRC, "calls.cpp")])
 
 
 def _build_calls() -> None:
     """Compile the argument checks of the E2M1 calls against torch's headers."""
     import torch
     root = os.path.dirname(os.path.abspath(torch.__file__))
-    tmp = CALLS + ".tmp"
+    calls = calls_path()
+    tmp = calls + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-isystem", os.path.join(root, "include"),
@@ -60,14 +75,18 @@ def _build_calls() -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed for calls.cpp:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, CALLS)
+    os.replace(tmp, calls)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile and link the library if needed; return its path."""
-    if not force and not _stale():
-        return LIB
+    """Compile and link the library, and the binding's argument checks, if needed;
+    return the library's path."""
+    stale, calls_stale = force or _stale(), force or _calls_stale()
     os.makedirs(OUT_DIR, exist_ok=True)
+    if not stale:
+        if calls_stale:
+            _build_calls()
+        return LIB
     nvcc = _nvcc()
     objs = []
 
@@ -82,9 +101,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 2)) as ex:
-        calls = ex.submit(_build_calls)
+        calls = ex.submit(_build_calls) if calls_stale else None
         objs = list(ex.map(compile_one, _sources()))
-        calls.result()
+        if calls is not None:
+            calls.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
