@@ -5,7 +5,9 @@ shared library with the CUDA runtime linked statically; beside them the host
 compiler builds ``_lib/_calls.<interpreter>-torch<version>.so``
 (``csrc/calls.cpp``), the Python binding's argument checks for the E2M1 calls,
 against this interpreter and its torch.  Rebuilds the one or the other only when it
-is missing or a source or header of it is newer.
+is missing or a source or header of it is newer.  The library needs nvcc alone:
+without torch, its headers or Python's the checks are left out (with a warning where
+there is a torch to bind), and the E2M1 calls from Python raise.
 """
 
 from __future__ import annotations
@@ -16,6 +18,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -56,8 +59,11 @@ def _stale() -> bool:
                   glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
-def _calls_stale() -> bool:
-    return _older(calls_path(), [os.path.join(CSRC, "calls.cpp")])
+def _calls_stale(force: bool) -> bool:
+    try:
+        return _older(calls_path(), [os.path.join(CSRC, "calls.cpp")]) or force
+    except ImportError:                                  # no torch: nothing to bind
+        return False
 
 
 def _build_calls() -> None:
@@ -78,14 +84,21 @@ def _build_calls() -> None:
     os.replace(tmp, calls)
 
 
+def _try_build_calls() -> None:
+    try:
+        _build_calls()
+    except (RuntimeError, OSError) as e:
+        warnings.warn(f"the E2M1 calls are not available from Python: {e}", RuntimeWarning)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     """Compile and link the library, and the binding's argument checks, if needed;
     return the library's path."""
-    stale, calls_stale = force or _stale(), force or _calls_stale()
     os.makedirs(OUT_DIR, exist_ok=True)
-    if not stale:
+    calls_stale = _calls_stale(force)
+    if not force and not _stale():
         if calls_stale:
-            _build_calls()
+            _try_build_calls()
         return LIB
     nvcc = _nvcc()
     objs = []
@@ -101,7 +114,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 2)) as ex:
-        calls = ex.submit(_build_calls) if calls_stale else None
+        calls = ex.submit(_try_build_calls) if calls_stale else None
         objs = list(ex.map(compile_one, _sources()))
         if calls is not None:
             calls.result()

@@ -1,8 +1,10 @@
 """The build of the library and of the binding's compiled checks (no compiler is run
-here): the checks are those of this interpreter and this torch."""
+here): the checks are those of this interpreter and this torch, and the library does
+not depend on them."""
 
 import os
 import subprocess
+import sys
 import types
 
 import pytest
@@ -74,6 +76,24 @@ def test_checks_of_another_torch_are_not_loaded(monkeypatch):
     monkeypatch.setattr(torch, "__version__", "0.0.1")
     with pytest.raises(ImportError, match="not built"):
         B._load_calls()
+
+
+def test_the_library_is_built_without_the_checks(tree):
+    tree.bad = "calls.cpp"
+    with pytest.warns(RuntimeWarning, match="Python.h"):
+        assert bld.build() == bld.LIB
+    assert os.path.exists(bld.LIB)
+    tree.commands.clear()
+    tree.bad = ""
+    bld.build()                                           # tried again, and only that
+    assert built(tree, "calls.cpp") == 1 and built(tree, "decode.cu") == 0
+
+
+def test_the_library_is_built_without_torch(tree, monkeypatch):
+    monkeypatch.setitem(sys.modules, "torch", None)
+    assert bld.build() == bld.LIB
+    assert os.path.exists(bld.LIB) and built(tree, "decode.cu") == 1
+    assert built(tree, "calls.cpp") == 0
 
 
 def test_a_failing_library_is_an_error(tree):
