@@ -126,11 +126,10 @@ struct Cfg {
   static constexpr int kWarps = W;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kRows = 8 * NT;
-  static constexpr int kPair = 2;                        // blocks per stage
+  using Stage = E2m1Stage<D>;
+  static constexpr int kPair = Stage::kPair;
   static constexpr int kPairKeys = kPair * kBlock;
-  // stage: K codes of both blocks, V codes, K scales, V scales
-  static constexpr int kStageBytes = 2 * kPair * P::kBytes;
-  static constexpr int kScaleOff = 2 * kPair * P::kCodes;
+  static constexpr int kStageBytes = Stage::kBytes;
   static constexpr int kStages = 3;
   static constexpr int kRing = kWarps * kStages * kStageBytes;
   static constexpr int kMerge = kWarps * kRows * (D + 3) * 4;
@@ -138,21 +137,15 @@ struct Cfg {
   static constexpr int kCtas = W <= 6 ? 2 : 1;           // per SM
 };
 
-// Where a merge row keeps its 16-byte chunks: position = chunk ^ this.
-template <int D>
-__device__ __forceinline__ int chunk_swizzle(int row) {
-  return D == 128 ? (row >> 1) & 3 : ((row >> 1) & 1) | ((row & 4));
-}
-
-// What a CTA does for its request: the row tile's keys [kv_lo, kv_hi), and the
-// blocks [b_beg, b_end) of its split.
+// What a CTA does for its request: the row tile's keys, and the blocks of its split.
 struct TileRange {
   static constexpr int kRun = 0, kNothing = 1, kBad = 2;
-  int state, splits, kv_lo, kv_hi, b_beg, b_end;
+  int state, splits;
+  KeyRange keys;
 };
 __device__ __forceinline__ TileRange tile_range(const AttnArgs& a, int q0, int q1, int L, int split,
                                                 int rho0, int rows_per_tile) {
-  TileRange t = {TileRange::kNothing, 1, 0, 0, 0, 0};
+  TileRange t = {TileRange::kNothing, 1, {0, 0, 0, 0}};
   const int n = q1 - q0;
   if (n == 0) return t;
   if (n < 0 || q0 < 0 || q1 > a.num_tokens || n > L || n > a.max_query_len ||
@@ -168,13 +161,7 @@ __device__ __forceinline__ TileRange tile_range(const AttnArgs& a, int q0, int q
   const int i_last = (min(rho0 + rows_per_tile, rows_total) - 1) / a.group;
   t.state = TileRange::kRun;
   t.splits = decode_class ? a.num_splits : 1;
-  t.kv_hi = a.causal ? L - n + i_last + 1 : L;
-  t.kv_lo = a.window > 0 ? max(0, L - n + i_first - a.window + 1) : 0;
-  const int blk_lo = t.kv_lo / kBlock;
-  const int nb = (t.kv_hi + kBlock - 1) / kBlock - blk_lo;
-  const int per = (nb + t.splits - 1) / t.splits;
-  t.b_beg = blk_lo + min(nb, split * per);
-  t.b_end = blk_lo + min(nb, (split + 1) * per);
+  t.keys = key_range(L, n, a.causal, a.window, i_first, i_last, t.splits, split);
   return t;
 }
 
@@ -185,6 +172,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, W>::kThreads, (Cfg<D, NT, W>::kCtas
     decode_e2m1_kernel(const AttnArgs a) {
   using C = Cfg<D, NT, W>;
   using P = E2m1Page<D>;
+  using Stage = E2m1Stage<D>;
   constexpr int kKWords = D / 32;                        // code words of a lane's K row part
   constexpr int kVWords = D / 64;                        // code words of a lane's V row part
   constexpr int kMT = D / 16;                            // 16-dim tiles of O^T, MMAs of a key block
@@ -220,9 +208,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, W>::kThreads, (Cfg<D, NT, W>::kCtas
   const int nrows = min(R, rows_total - rho0);
   const int i_first = rho0 / group, i_last = (rho0 + nrows - 1) / group;
   const int splits = range.splits;
-  const int kv_hi = range.kv_hi, kv_lo = range.kv_lo;
-  const int b_beg = range.b_beg, b_end = range.b_end;
-  const int npairs = (b_end - b_beg + C::kPair - 1) / C::kPair;
+  const int kv_hi = range.keys.kv_hi, kv_lo = range.keys.kv_lo;
+  const int b_end = range.keys.b_end;
   // keys every row of the tile sees: [in_lo, in_hi)
   const int in_hi = min(a.causal ? L - n + i_first + 1 : L, b_end * kBlock);
   const int in_lo = a.window > 0 ? max(0, L - n + i_last - a.window + 1) : 0;
@@ -232,24 +219,22 @@ __global__ void __launch_bounds__(Cfg<D, NT, W>::kThreads, (Cfg<D, NT, W>::kCtas
   uint8_t* const ring = smem + warp * (C::kStages * C::kStageBytes);
   uint8_t* const ring_end = ring + C::kStages * C::kStageBytes;
   const int32_t* table = a.block_table + static_cast<int64_t>(r) * a.max_blocks_per_seq;
-  const int npw = npairs > warp ? (npairs - warp - 1) / C::kWarps + 1 : 0;
+  const int npw = warp_pairs(range.keys, warp, C::kWarps);
   const uint32_t page_stride = static_cast<uint32_t>(a.hkv) * P::kBytes;
   const uint8_t* kbase = static_cast<const uint8_t*>(a.k_cache) + kvh * P::kBytes;
   const uint8_t* vbase = static_cast<const uint8_t*>(a.v_cache) + kvh * P::kBytes;
-  // this lane's chunk of the scale areas: of page p = lane / kSC (K of both
-  // blocks, V of both)
-  constexpr int kSC = P::kScales / 16;
-  const bool has_scales = lane < 2 * C::kPair * kSC;
+  // this lane's chunk of the scale areas
+  const bool has_scales = lane < Stage::kScaleLanes;
   const uint8_t* sbase =
-      (lane / kSC < C::kPair ? kbase : vbase) + P::kCodes + (lane % kSC) * 16;
-  kbase += lane * 16;
-  vbase += lane * 16;
+      (Stage::scale_page(lane) < C::kPair ? kbase : vbase) + Stage::scale_source(lane);
+  kbase += Stage::code_chunk(lane, 0);
+  vbase += Stage::code_chunk(lane, 0);
   // table entries of 16 consecutive pairs of the warp, two a lane pair; 0 (a
   // page that exists) stands for a block past the run, whose keys are masked,
   // and for an entry outside the cache, whose rows are unspecified
   auto load_ids = [&](int k0) -> uint32_t {
     const int k = k0 + (lane >> 1);
-    const int blk = b_beg + C::kPair * (warp + k * C::kWarps) + (lane & 1);
+    const int blk = pair_block(range.keys, warp, C::kWarps, k) + (lane & 1);
     if (k >= npw || blk >= b_end) return 0;
     const int32_t id = __ldg(table + blk);
     if (id < 0 || id >= a.num_blocks) {
@@ -265,8 +250,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, W>::kThreads, (Cfg<D, NT, W>::kCtas
   // same bytes.
   constexpr int kNewUnits = 2 * P::kRowScales;           // scale blocks of a token's K and V row
   static_assert(kDecodeMaxQ * kNewUnits <= C::kThreads, "a thread per scale block");
-  const int new_lo = max(L - n, max(kv_lo, b_beg * kBlock));
-  const int new_hi = a.fuse_write ? min(kv_hi, b_end * kBlock) : 0;
+  const int new_lo = new_keys_lo(L, n, range.keys);
+  const int new_hi = a.fuse_write ? new_keys_hi(range.keys) : 0;
   const bool stores = static_cast<int>(threadIdx.x) < (new_hi - new_lo) * kNewUnits;
   const int new_b = threadIdx.x % P::kRowScales;
   const bool new_v = (threadIdx.x / P::kRowScales) & 1;
@@ -283,27 +268,27 @@ __global__ void __launch_bounds__(Cfg<D, NT, W>::kThreads, (Cfg<D, NT, W>::kCtas
   auto issue = [&](int k) {
     if (k < npw) {
       if ((k & 15) == 0 && k > 0) ids = load_ids(k);
-      const uint32_t to = smem_u32(put) + lane * 16;
+      const uint32_t to = smem_u32(put) + Stage::code_chunk(lane, 0);
 #pragma unroll
       for (int j = 0; j < C::kPair; ++j) {
         const uint64_t off = static_cast<uint64_t>(__shfl_sync(0xffffffffu, ids, 2 * (k & 15) + j)) *
                              page_stride;
 #pragma unroll
-        for (int c = 0; c < P::kCodes / 512; ++c) {
-          cp_async16(to + j * P::kCodes + c * 512, kbase + off + c * 512);
-          cp_async16(to + (C::kPair + j) * P::kCodes + c * 512, vbase + off + c * 512);
+        for (int c = 0; c < Stage::kCodeChunks; ++c) {
+          cp_async16(to + Stage::codes(0, j) + c * 512, kbase + off + c * 512);
+          cp_async16(to + Stage::codes(1, j) + c * 512, vbase + off + c * 512);
         }
       }
-      const uint32_t id = __shfl_sync(0xffffffffu, ids, 2 * (k & 15) + ((lane / kSC) & 1));
+      const uint32_t id = __shfl_sync(0xffffffffu, ids, 2 * (k & 15) + (Stage::scale_page(lane) & 1));
       if (has_scales)
-        cp_async16(to + C::kScaleOff, sbase + static_cast<uint64_t>(id) * page_stride);
+        cp_async16(smem_u32(put) + Stage::scale_dest(lane), sbase + static_cast<uint64_t>(id) * page_stride);
       put += C::kStageBytes;
       if (put == ring_end) put = ring;
     }
     cp_async_commit();
   };
   const int early =                                      // the warp's first pair that has to wait
-      new_lo < new_hi ? (new_lo / kBlock - b_beg - C::kPair * warp) / (C::kPair * C::kWarps) : npw;
+      new_lo < new_hi ? waiting_pair(range.keys, new_lo, warp, C::kWarps) : npw;
 #pragma unroll
   for (int k = 0; k < C::kStages - 1; ++k)
     if (k < early) issue(k);
@@ -377,8 +362,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, W>::kThreads, (Cfg<D, NT, W>::kCtas
     }
   }
 
-  const int ka = (g8 & 1) ? ((g8 >> 1) ^ 1) + 4 : g8 >> 1;   // kappa(g8); the lane's other key + 8
-  const int kv[4] = {t4, (t4 ^ 1) + 4, t4 + 8, (t4 ^ 1) + 12};
+  const int ka = score_key(lane);                        // kappa(g8); the lane's other key + 8
   float oacc[NT][kMT][4];
   float ref[NT][2], l[NT][2], lr[NT][4];
 #pragma unroll
@@ -406,10 +390,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, W>::kThreads, (Cfg<D, NT, W>::kCtas
 #pragma unroll
         for (int c = 0; c < 4; ++c) x[j][nt][c] = 0.f;
       uint32_t wa[kKWords], wb[kKWords], sa[2], sb[2];
-      const uint8_t* row = st + j * P::kCodes + ka * P::kRowCodes + t4 * (D / 8);
+      const uint8_t* row = st + Stage::codes(0, j) + k_codes_at<D>(lane);
       load_words<kKWords>(wa, row);
       load_words<kKWords>(wb, row + 8 * P::kRowCodes);
-      const uint8_t* srow = st + C::kScaleOff + j * P::kScales + ka * P::kRowScales + t4 * (D / 64);
+      const uint8_t* srow = st + Stage::scales(0, j) + k_scales_at<D>(lane);
       if constexpr (D == 128) {
         const uint32_t ha = scales2_to_f16x2(*reinterpret_cast<const uint16_t*>(srow));
         const uint32_t hb =
@@ -452,7 +436,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, W>::kThreads, (Cfg<D, NT, W>::kCtas
   }
   for (int k = 0; k < npw; ++k) {
     issue(k + C::kStages - 1);                           // (into the stage that step k - 1 left)
-    const int key0 = (b_beg + C::kPair * (warp + k * C::kWarps)) * kBlock;
+    const int key0 = pair_block(range.keys, warp, C::kWarps, k) * kBlock;
     const bool edge = key0 + C::kPairKeys > in_hi || key0 < in_lo;
     // this lane's V scales: block g8 D / 128 of its four keys of both blocks
     uint32_t cs[C::kPair][4];
@@ -460,8 +444,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, W>::kThreads, (Cfg<D, NT, W>::kCtas
     for (int j = 0; j < C::kPair; ++j)
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        cs[j][c] = st[C::kScaleOff + (C::kPair + j) * P::kScales + kv[c] * P::kRowScales +
-                      g8 * D / 128];
+        cs[j][c] = st[Stage::scales(1, j) + v_scales_at<D>(lane, c)];
     if (edge) {
       // p is 0 outside a row's keys, and so must p v be whatever a hidden slot
       // holds: a scale outside the tile's keys, or a NaN one that some row of
@@ -478,7 +461,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, W>::kThreads, (Cfg<D, NT, W>::kCtas
           }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const int key = key0 + j * kBlock + kv[c];
+          const int key = key0 + j * kBlock + value_key(lane, c);
           const bool nan = (cs[j][c] & 0x7F) == 0x7F;
           const bool in = key < cap && key >= kv_lo;
           bad = bad || (nan && in);
@@ -493,8 +476,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, W>::kThreads, (Cfg<D, NT, W>::kCtas
           for (int jc = 0; jc < 4 * C::kPair; ++jc) {
             const int j = jc / 4, c = jc % 4;
             const uint32_t v = __shfl_sync(0xffffffffu, cs[j][c], g8 * 4 + q);
-            const int key =
-                key0 + j * kBlock + ((c & 1) ? (q ^ 1) + 4 : q) + (c >> 1) * 8;
+            const int key = key0 + j * kBlock + value_key(q, c);
             if (v == 0x100) {
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
@@ -578,10 +560,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, W>::kThreads, (Cfg<D, NT, W>::kCtas
     // O^T += V^T P^T
 #pragma unroll
     for (int j = 0; j < C::kPair; ++j) {
-      const uint8_t* vrow = st + (C::kPair + j) * P::kCodes + g8 * (D / 16);
+      const uint8_t* vrow = st + Stage::codes(1, j);
       uint32_t vw[4][kVWords];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) load_words<kVWords>(vw[c], vrow + kv[c] * P::kRowCodes);
+      for (int c = 0; c < 4; ++c) load_words<kVWords>(vw[c], vrow + v_codes_at<D>(lane, c));
       const uint32_t s01 = vs[j][0], s23 = vs[j][1];
 #pragma unroll
       for (int w = 0; w < kVWords; ++w) {
@@ -632,7 +614,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, W>::kThreads, (Cfg<D, NT, W>::kCtas
         float4* row = reinterpret_cast<float4*>(aw + (warp * R + rho) * D);
 #pragma unroll
         for (int i = 0; i < kMT; i += 2)
-          row[(g8 * (D / 32) + i / 2) ^ chunk_swizzle<D>(rho)] =
+          row[merge_chunk<D>(rho, g8 * (D / 32) + i / 2)] =
               make_float4(oacc[nt][i][c], oacc[nt][i][c + 2], oacc[nt][i + 1][c],
                           oacc[nt][i + 1][c + 2]);
       }
@@ -652,7 +634,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, W>::kThreads, (Cfg<D, NT, W>::kCtas
       const float f = ex2(mw[w * R + rho] - M);
       lsum = fmaf(f, lw[w * R + rho], lsum);
       lnorm = fmaf(f, lrw[w * R + rho], lnorm);
-      const int chunk = (lane * kDPL / 4) ^ chunk_swizzle<D>(rho);
+      const int chunk = merge_chunk<D>(rho, lane * kDPL / 4);
       const float* src = aw + (w * R + rho) * D + chunk * 4 + lane * kDPL % 4;
 #pragma unroll
       for (int e = 0; e < kDPL; ++e) o[e] = fmaf(f, src[e], o[e]);

@@ -12,18 +12,11 @@
 #pragma once
 
 #include "common.cuh"
+#include "e2m1_index.h"
 
 namespace pkv {
 
-constexpr int kQuant = 16;                               // elements per scale
-template <int D>
-struct E2m1Page {
-  static constexpr int kRowCodes = D / 2;                // code bytes of a token row
-  static constexpr int kRowScales = D / kQuant;          // scale bytes of a token row
-  static constexpr int kCodes = kBlock * kRowCodes;
-  static constexpr int kScales = kBlock * kRowScales;
-  static constexpr int kBytes = kCodes + kScales;        // 9 D
-};
+static_assert(kPageTokens == kBlock, "a page is a cache block");
 
 // Eight E2M1 codes (a word, element 0 in the low nibble) -> four f16 pairs.
 __device__ __forceinline__ void e2m1x8_to_f16x2x4(uint32_t w, uint32_t (&r)[4]) {

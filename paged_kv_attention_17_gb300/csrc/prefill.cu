@@ -82,6 +82,7 @@ constexpr int kQRows = 128;          // query rows per tile
 constexpr int kKeys = 128;           // keys per K/V tile (8 blocks)
 constexpr int kStages = 2;
 constexpr int kHalf = 16384;         // 64 columns of a 128-row 16-bit tile (128-byte rows)
+static_assert(kHalf == kWidenHalf && kKeys == 128, "the widening's tile");
 constexpr int kCodeBytes = kKeys * 128;   // one K (or V) tile of E4M3 codes at head_dim 128
 static_assert(kCodeBytes == kHalf, "a code tile fills the second half of its ring slot");
 
@@ -100,7 +101,6 @@ __host__ __device__ constexpr int num_bars(bool f8) { return 1 + 4 * kStages + 6
 __host__ __device__ constexpr int off_misc(bool f8) { return off_bar(f8) + num_bars(f8) * 8; }
 // E2M1: notes of NaN V scales in edge tiles, [edge tile][block of a row][key / 32],
 // after one word that says whether there is any
-constexpr int kEdgeTiles = 6;                             // 3 at each end of a key range
 constexpr int kNoteWords = 1 + kEdgeTiles * 8 * (kKeys / 32);
 __host__ __device__ constexpr int off_notes() { return off_misc(true) + 32; }
 __host__ __device__ constexpr int smem_alloc(bool f8) {
@@ -492,9 +492,7 @@ __global__ void __launch_bounds__(threads_for(KV != kKvBf16), 1)
     const int key0 = (kt_base + kt) * kKeys;
     const int lim_first = a.causal ? min(L - n + i0 + 1, L) : L;
     const int lo_last = a.window > 0 ? L - n + i_hi - a.window + 1 : 0;
-    if (key0 + kKeys > lim_first && ntk - 1 - kt < kEdgeTiles / 2) return ntk - 1 - kt;
-    if (key0 < lo_last && kt < kEdgeTiles / 2) return kEdgeTiles / 2 + kt;
-    return -1;
+    return edge_place(kt, ntk, key0, lim_first, lo_last);
   };
   if constexpr (E2)
     for (int i = threadIdx.x; i < kNoteWords; i += kThreads) notes[i] = 0;
@@ -704,9 +702,9 @@ __global__ void __launch_bounds__(threads_for(KV != kKvBf16), 1)
       // is written, which may lie over codes.
       constexpr int kUnits = kKeys * Page::kRowScales / 64;
       const int ct = threadIdx.x - 10 * 32;
-      const int b = ct % Page::kRowScales, r0 = ct / Page::kRowScales;
-      constexpr int kStep = 64 / Page::kRowScales;       // rows from a unit to the next: 8 or 16
-      const int r7 = r0 & 7, c0 = 2 * (b & 3), second = b >> 2;
+      const int b = widen_block<D>(ct), r0 = widen_row<D>(ct);
+      const int kStep = widen_step<D>();
+      const bool swapped = widen_word(b, 0) != 0;
       for (int kt = 0; ok && kt < ntk; ++kt) {
         const int st = kt % kStages;
         const int key0 = (kt_base + kt) * kKeys;
@@ -739,19 +737,15 @@ __global__ void __launch_bounds__(threads_for(KV != kKvBf16), 1)
             ok = false;
             break;
           }
-          // chunk c0 + second of the block takes its word second, c0 + 1 - second
-          // the other
-          const uint32_t dst0 =
-              slot_base + second * kHalf + r0 * 128 + (((c0 + second) ^ r7) << 4);
-          const uint32_t dst1 =
-              slot_base + second * kHalf + r0 * 128 + (((c0 + 1 - second) ^ r7) << 4);
+          const uint32_t dst0 = slot_base + widen_to(b, r0, 0);
+          const uint32_t dst1 = slot_base + widen_to(b, r0, 1);
           auto widen = [&](int i) {
             const uint32_t s2 = scales2_to_f16x2(sc[i] * 0x0101u);
             uint32_t v[4];
-            e2m1x8_to_f16x2x4(second ? cw[i].y : cw[i].x, v);
+            e2m1x8_to_f16x2x4(swapped ? cw[i].y : cw[i].x, v);
             sts128(dst0 + i * kStep * 128, make_uint4(mul_f16x2(v[0], s2), mul_f16x2(v[1], s2),
                                                       mul_f16x2(v[2], s2), mul_f16x2(v[3], s2)));
-            e2m1x8_to_f16x2x4(second ? cw[i].x : cw[i].y, v);
+            e2m1x8_to_f16x2x4(swapped ? cw[i].x : cw[i].y, v);
             sts128(dst1 + i * kStep * 128, make_uint4(mul_f16x2(v[0], s2), mul_f16x2(v[1], s2),
                                                       mul_f16x2(v[2], s2), mul_f16x2(v[3], s2)));
           };
