@@ -71,7 +71,7 @@ def test_several_tokens_on_a_long_context(n, hq, hkv, d, window):
 def test_a_chunk_among_requests_of_several_tokens(window, splits):
     rng = np.random.default_rng(65)
     lens = [(int(rng.integers(300, 1500)), int(rng.integers(2, 5))) for _ in range(31)]
-    step(Batch(lens[:15] + [(1300, 400)] + lens[15:], 32, 8, 128, seed=66, window=window), splits, 67)
+    step(Batch(lens[:15] + [(1300, 400)] + lens[15:], 16, 4, 128, seed=66, window=window), splits, 67)
 
 
 @pytest.mark.parametrize("hq, hkv", [(128, 1), (64, 2)])
