@@ -221,7 +221,8 @@ int split_rule(int num_seqs, int max_query_len, int max_seq_len, int num_q_heads
                                                  static_cast<int64_t>(num_seqs) * num_kv_heads,
                                                  nblk, sms)
                      : decode_rows_per_tile(group, qd, false);
-  const int64_t units = static_cast<int64_t>(num_seqs) * num_kv_heads * ((group * qd + R - 1) / R);
+  const int64_t row_tiles = (static_cast<int64_t>(group) * qd + R - 1) / R;
+  const int64_t units = static_cast<int64_t>(num_seqs) * num_kv_heads * row_tiles;
   // decode CTA slots of the device (two per SM for the tensor-core build);
   // 7/8 of them leave room for the combine and the next launch's prologue
   // (decode at context 8192, 8 KV heads, bf16, 152 SMs: 16 splits take
