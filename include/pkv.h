@@ -35,8 +35,10 @@
  *     num_kv_heads; dtype PKV_F32 or PKV_BF16 (same dtype for Q, K, V and
  *     the output), or an 8-bit E4M3 cache with bf16 Q and output through the
  *     _e4m3 entry points, or a 4-bit E2M1 cache of pages (pkv_write_e2m1)
- *     through the _e2m1 ones.  Arithmetic is fp32 with fp32 accumulation (the
- *     tensor-core prefill rounds P to bf16 for its P.V product).
+ *     through the _e2m1 ones.  Arithmetic is fp32 with fp32 accumulation; the
+ *     tensor-core prefill rounds P to bf16 for its P.V product.  On tensor cores
+ *     over E4M3 and E2M1 codes q rows are scaled and narrowed and P is rounded to
+ *     f16, as those entry points say.
  *
  * Entry points: pkv_write / pkv_write_e4m3 / pkv_write_e2m1 (slot-mapped write),
  * pkv_read_e2m1 (cached rows read back), pkv_stage_inputs
@@ -437,7 +439,10 @@ pkv_status pkv_write_attention_varlen_e4m3(
  * are widened exactly to f16; each q row enters as f16 scaled by a power of two
  * (its largest magnitude in [2^14, 2^15): exact for every element within 2^31
  * of it); both contractions run on tensor cores with fp32 accumulation, P
- * rounded to f16 for P.V.  Requests with n > PKV_DECODE_MAX_QLEN take the
+ * rounded to f16 for P.V (decode tiles divide by the sum of the rounded P, prefill
+ * tiles by the sum of P before rounding: within 2^-11 of one another).  A row that
+ * sees a NaN score has a NaN output and log-sum-exp at any num_splits; one that
+ * sees a NaN V scale, NaN in its 16 dims alone.  Requests with n > PKV_DECODE_MAX_QLEN take the
  * tcgen05 prefill tiles (pages widened in shared memory) at a positive
  * softmax_scale without a window below 128 keys, else the decode kernel's 16-row
  * tiles; PKV_ERR_UNSUPPORTED for more than 65535 KV heads, on those tiles for

@@ -34,13 +34,15 @@
 //   free of bank conflicts (D 128), and V's at two ways.
 //
 // What bounds it.  Bytes per (key, KV head): 2 x 9 D / 16.  Two contexts of 128K
-// keys (302 MB, 32 / 8 heads of 128) take 57 us, 5.3 TB/s with the combine, 78% of
+// keys (302 MB, 32 / 8 heads of 128) take 58.4 us, 5.2 TB/s with the combine, 76% of
 // the measured copy rate; the same loads without arithmetic 55 us.  64 requests
-// of 512 to 4096 keys (169 MB) take 41.4 us, 42.4 with their new rows written in
-// the same launch; their loads alone 32: 267 instructions a block and KV head
-// (64 code conversions, 64 scale products, 17 MMAs), ALU pipe 50% busy, and CTAs
-// of unequal length.  One request of 8192 keys takes 8.8 us: latency (metadata,
-// table, first loads, 2 pairs a warp, merge, combine).
+// of 512 to 4096 keys (169 MB) take 41.7 us, 42.5 with their new rows written in
+// the same launch; their loads alone 32.  512 CTAs of unequal length share 304
+// slots: a second wave begins with its table and first loads again, and the SMs are
+// idle for a quarter of the launch; while they run, 50% of the issue slots and 42% of
+// the ALU pipe are taken (267 instructions a block and KV head: 64 code conversions,
+// 64 scale products, 17 MMAs).  One request of 8192 keys takes 8.9 us: latency
+// (metadata, table, first loads, 2 pairs a warp, merge, combine).
 #include <atomic>
 #include <cmath>
 

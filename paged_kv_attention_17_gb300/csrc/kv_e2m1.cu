@@ -12,7 +12,7 @@
 // rounding.  A block holding a NaN gets the NaN scale, so the NaN is not lost.
 // Bytes per token: 2 tensors x H x D x (input size + 9 / 16).  A thread takes a
 // block of one tensor, the next one's inputs loaded ahead.  8192 tokens of 8 heads
-// of 128 in bf16 take 11.8 us (43.1 MB, 3.65 TB/s, 54% of the measured copy
+// of 128 in bf16 take 12.0 us (43.1 MB, 3.6 TB/s, 53% of the measured copy
 // rate); the same loads and stores without the quantising take 8.8, so latency
 // and the arithmetic (eight packed fp32 operations a pair of elements for the two
 // quotients) bound it, not HBM.  With plain divisions it took 18.7 us, with the
@@ -21,7 +21,7 @@
 // Read.  The inverse: RN32(t * (s * code)), s * code exact, then rounded to the
 // output type.  Bytes per row: 2 tensors x H x D x (9 / 16 + output size).  A
 // thread takes 16 bytes of output of both tensors, striding over the rows: 64
-// contexts (144 thousand rows) of 8 heads of 128 to bf16 take 118.8 us (734 MB,
+// contexts (144 thousand rows) of 8 heads of 128 to bf16 take 119.0 us (734 MB,
 // 6.17 TB/s, 91% of the measured copy rate), bound by HBM; a thread per 16 bytes
 // of one tensor without the stride took 211 us.
 #include "e2m1.cuh"
