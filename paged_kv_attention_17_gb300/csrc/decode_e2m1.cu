@@ -38,9 +38,9 @@
 // the measured copy rate; the same loads without arithmetic 55 us.  64 requests
 // of 512 to 4096 keys (169 MB) take 41.7 us, 42.5 with their new rows written in
 // the same launch; their loads alone 32.  512 CTAs of unequal length share 304
-// slots: a second wave begins with its table and first loads again, and the SMs are
-// idle for a quarter of the launch; while they run, 50% of the issue slots and 42% of
-// the ALU pipe are taken (267 instructions a block and KV head: 64 code conversions,
+// slots: a second wave begins with its table and first loads again, and by itself
+// the launch leaves the SMs idle for a quarter of its time; while they run, 50% of the
+// issue slots and 43% of the ALU pipe are taken (267 instructions a block and KV head: 64 code conversions,
 // 64 scale products, 17 MMAs).  One request of 8192 keys takes 8.9 us: latency
 // (metadata, table, first loads, 2 pairs a warp, merge, combine).
 #include <atomic>
