@@ -40,9 +40,9 @@
 // the same launch; their loads alone 32.  512 CTAs of unequal length share 304
 // slots: a second wave begins with its table and first loads again, and by itself
 // the launch leaves the SMs idle for a quarter of its time; while they run, 50% of the
-// issue slots and 43% of the ALU pipe are taken (267 instructions a block and KV head: 64 code conversions,
-// 64 scale products, 17 MMAs).  One request of 8192 keys takes 8.9 us: latency
-// (metadata, table, first loads, 2 pairs a warp, merge, combine).
+// issue slots and 43% of the ALU pipe are taken (267 instructions a block and KV head:
+// 64 code conversions, 64 scale products, 17 MMAs).  One request of 8192 keys takes
+// 8.9 us: latency (metadata, table, first loads, 2 pairs a warp, merge, combine).
 #include <atomic>
 #include <cmath>
 
