@@ -55,9 +55,10 @@
 // 7 below the row's maximum), so that f16's subnormals start 2^21 under a row's
 // largest p.  l sums p before that rounding (as over E4M3; the E2M1 decode tiles sum
 // the rounded p by one more MMA): the weights then sum to 1 within 2^-11, an eighth
-// of what the output's rounding to bf16 may be off by.  A NaN scale of V in a tile that crosses a mask edge is widened to
-// zeros and noted: the rows that see its key take the NaN at the end, the rows
-// that do not are untouched (0 * NaN would reach them through the MMA).  Interior
+// of what the output's rounding to bf16 may be off by.  A NaN scale of V in a tile
+// that crosses a mask edge is widened to zeros and noted: the rows that see its key
+// take the NaN at the end, the rows that do not are untouched (0 * NaN would reach
+// them through the MMA).  Interior
 // tiles take a branch-free widening (8192 causal tokens, 32 / 8 heads of 128: 453
 // us, 1213 TFLOP/s; bf16 427 us, E4M3 466).
 //
