@@ -349,8 +349,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j.rows == 0) break;
         const int32_t* table = a.block_table + static_cast<int64_t>(j.request) * a.max_blocks_per_seq;
         const int blocks = min(j.blocks, j.tile1 * kParts);
-        // -2: behind the keys
-        auto entry = [&](int b) { return b < blocks ? __ldg(table + b) : -2; };
+        // (-1 behind the keys, where the table is not looked at)
+        auto entry = [&](int b) { return b < blocks ? __ldg(table + b) : -1; };
         // the tiles after the next are brought into L2 meanwhile: more in flight than shared
         // memory has room for (not before the block's first tile has landed: every block
         // waits for that one)
@@ -370,7 +370,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             hint(next);
           }
           if (it >= kStages && !(ok = poll(&empty[st * 2 + g / 2], ((it / kStages) - 1) & 1))) break;
-          if (now >= 0 && now < a.num_blocks) {
+          const Page page = page_of(b, blocks, now, a.num_blocks);
+          if (page == Page::kLoad) {
             uint8_t* to = smem + kOffTiles + st * kTile + g * kPart;
             mbar_arrive_expect_tx(&full[st], kPart);
             tma_load_3d(to, &cmap, &full[st], 0, now * kBlock, 0, policy);
@@ -378,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             // behind the keys (its scores are hidden and O does not take it), or no block of
             // the cache (the row is unspecified)
-            if (now != -2) raise_flag(a.flag, PKV_FLAG_BAD_BLOCK);
+            if (page == Page::kBad) raise_flag(a.flag, PKV_FLAG_BAD_BLOCK);
             mbar_arrive(&full[st]);
           }
           if (it >= kStages) hint(later);

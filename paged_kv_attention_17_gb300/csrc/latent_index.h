@@ -119,6 +119,14 @@ struct LatentWalk {
   }
 };
 
+// What is done about the block at place b of a unit's keys, which end in place `blocks` - 1:
+// entry is what the block table holds there.  By the place, as an entry may have any value.
+enum class Page { kLoad, kBehind, kBad };
+PKV_LATENT_INDEX Page page_of(int b, int blocks, int entry, int64_t num_blocks) {
+  if (b >= blocks) return Page::kBehind;
+  return entry >= 0 && entry < num_blocks ? Page::kLoad : Page::kBad;
+}
+
 // Partials: block c keeps the piece that begins inside a unit in slot 2 c, the piece that
 // a later block goes on with in slot 2 c + 1.
 PKV_LATENT_INDEX int piece_slot(int block, bool first) { return 2 * block + (first ? 1 : 0); }
