@@ -328,9 +328,10 @@ size_t pkv_latent_workspace_bytes(int device);
  *   softmax_scale  finite, > 0 (else PKV_ERR_UNSUPPORTED).
  *   workspace    >= pkv_latent_workspace_bytes(device) bytes, 256-byte aligned, of any
  *                contents; calls that may overlap on the GPU need one each.
- * What cache slots behind a context hold never reaches a row.  A row that sees a NaN or
- * +inf score is NaN; where it scores a row with an infinity -inf, elements of its output may
- * be NaN.  num_q_heads <= 4096, num_seqs <= 65535, num_tokens * num_q_heads and num_blocks
+ * What a row does not see never reaches it.  A row that sees a NaN or +inf score is NaN.  A
+ * score of -inf weighs 0: where such a key holds an infinity, that element of the rows that
+ * see it is NaN (0 times it); a row with no other scores is 0 elsewhere, its log-sum-exp
+ * -inf.  num_q_heads <= 4096, num_seqs <= 65535, num_tokens * num_q_heads and num_blocks
  * * 16 < 2^31 (else PKV_ERR_UNSUPPORTED); a context is at most 2^30 keys.  The rest as
  * pkv_attention_varlen.
  */

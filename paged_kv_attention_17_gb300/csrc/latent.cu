@@ -33,9 +33,10 @@
 // above it: p <= 2^8, and O is rescaled rarely.
 //
 // A hidden key's p is 0, but 0 times a NaN value is a NaN: in the tiles that cross a row's
-// limit, rows behind the unit's last key are zeroed, and so is a row whose scores are
-// non-finite for every query row (then it holds a NaN or an infinity, whose score makes
-// the rows that do see it NaN by themselves).
+// limit, keys behind the unit's last one are zeroed, and so is a key that some of the unit's
+// rows do not see and whose scores are non-finite for all of them (any key with a NaN or an
+// infinity is).  The rows that do see it are NaN by its score, unless that is -inf: then, as in
+// every other tile, only the elements that 0 times an infinity makes so (spoil).
 //
 // What bounds it.  HBM where a key meets few rows; from about 64 rows a key, shared memory: a
 // tile of 64 keys and 64 rows is 36 MMAs that read 4 KB each and 16 that read 6 KB, beside 72
@@ -88,6 +89,7 @@ static_assert(kOffTiles % 1024 == 0 && kOffP % 1024 == 0 && kOffMisc % 16 == 0 &
 constexpr int kTmemCols = 512;
 constexpr int kColO = 0, kColS = 256;
 constexpr float kSlack = 8.f;
+constexpr float kNoKeys = INFINITY;              // for the log-sum-exps of a piece without tiles
 // Tiles a block takes at least.  1 request of 8192 keys: 15.1 us with 1 (more pieces to
 // merge), 14.2 with 2, 15.3 with 3, 15.8 with 4.
 constexpr int kLeastPositions = 2;
@@ -219,6 +221,31 @@ struct Job {
   int pieces;                                    // of the unit, where it begins here
 };
 static_assert(sizeof(Job) <= 64, "pieces in shared memory");
+
+// NaN in the elements of a piece's output (bf16 rows, or fp32 partials) that a key of [key0,
+// key1) spoils, which some of its rows see and others do not: those where the key holds an
+// infinity or a NaN, of the rows that see it.  The key weighs 0 there.  (Rare, and so out of the
+// way: a thread looks its two dims up in the cache.)
+template <typename T>
+__device__ __noinline__ void spoil(T* to, T nan, const __nv_bfloat16* cache, const int32_t* table,
+                                   int64_t num_blocks, int hq, int lead, int first_row, int rows,
+                                   int key0, int key1, int dim0) {
+#pragma unroll 1
+  for (int key = key0; key < key1; ++key) {
+    const int block = __ldg(table + key / kBlock);
+    if (block < 0 || block >= num_blocks) continue;
+    const __nv_bfloat16* x = cache + (static_cast<int64_t>(block) * kBlock + key % kBlock) * kLatentRow;
+    // (row i of the request sees the keys below lead + i / hq)
+    const int64_t from = static_cast<int64_t>(key + 1 - lead) * hq - first_row;
+#pragma unroll 1
+    for (int dim = dim0; dim < kLatent; dim += 256) {
+      if ((__bfloat16_as_ushort(x[dim]) & 0x7F80u) != 0x7F80u) continue;
+#pragma unroll 1
+      for (int row = from > 0 ? static_cast<int>(from) : 0; row < rows; ++row)
+        to[static_cast<int64_t>(row) * kLatent + dim] = nan;
+    }
+  }
+}
 
 }  // namespace
 
@@ -527,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int slot = piece_slot(blockIdx.x, j.first != 0);
       if (j.pieces > 0) begun = Unsplit{row0, rows, j.pieces};
       if (j.tile0 >= j.tile1) {                            // (never a whole unit)
-        if (threadIdx.x < rows) ws_lse[lse_at(threadIdx.x, slot, gridDim.x)] = -INFINITY;
+        if (threadIdx.x < rows) ws_lse[lse_at(threadIdx.x, slot, gridDim.x)] = kNoKeys;
         continue;
       }
       const bool valid_a = ra < rows, valid_b = rb < rows;
@@ -538,6 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       const int lim_a = limit(min(ra, rows - 1)), lim_b = limit(min(rb, rows - 1));
       const int lim_min = limit(0), kv_len = limit(rows - 1);
+      bool spoilt = false;                                 // some rows see what others are spared
       float ma = -INFINITY, mb = -INFINITY, la = 0.f, lb = 0.f;
 #pragma unroll 1
       for (int kt = j.tile0; kt < j.tile1; ++kt, ++it) {
@@ -570,7 +598,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int first = 32 * half;
           const int held = min(j.blocks * kBlock - key0, kTileKeys) - first;
           const int seen = kv_len - key0 - first;
+          const int shown = lim_min - key0 - first;        // (to all rows)
           uint32_t zero = bad[half];
+          if (shown > 0) zero &= shown < 32 ? ~0u << shown : 0u;
+          if (seen < 32) zero &= seen <= 0 ? 0u : (1u << seen) - 1;
+          spoilt |= zero != 0;
           if (seen < 32) zero |= seen <= 0 ? 0xffffffffu : ~0u << seen;
           if (held < 32) zero &= held <= 0 ? 0u : (1u << held) - 1;
           const int slab = threadIdx.x % 64 / 8, odd = threadIdx.x / 64 % 2;
@@ -708,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       wait_o(it - 1, 1);
       tc::fence_after();
-      tc::sync_named(1, kSoftmax);
+      spoilt = tc::any_of(1, kSoftmax, spoilt);
       // (lane = dim, column = row; 16 rows at a time)
 #pragma unroll 1
       for (int c = 0; c < 8; ++c) {
@@ -746,6 +778,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (first + i < rows) to[i * kLatent] = f[i];
         }
       }
+      if (spoilt) {
+        __syncwarp();                                      // (behind the warp's stores)
+        const int32_t* table = a.block_table + static_cast<int64_t>(j.request) * a.max_blocks_per_seq;
+        const int key0 = max(lim_min, j.tile0 * kTileKeys), key1 = min(kv_len, j.tile1 * kTileKeys);
+        const int dim0 = half * 128 + w4 * 32 + lane;
+        if (whole)
+          spoil(a.out + row0 * kLatent, __ushort_as_bfloat16(0x7FFF), a.cache, table, a.num_blocks, a.hq,
+                j.lead, j.first_row, rows, key0, key1, dim0);
+        else
+          spoil(ws_o + static_cast<int64_t>(slot) * a.slot_rows * kLatent, __int_as_float(0x7FC00000), a.cache,
+                table, a.num_blocks, a.hq, j.lead, j.first_row, rows, key0, key1, dim0);
+      }
       tc::fence_before();
       tc::sync_named(1, kSoftmax);                         // (the factors are free again)
     }
@@ -782,13 +826,15 @@ struct Merge {
 };
 
 // The lanes' weights within each run of `Lanes` (a piece without keys, weight -1 here, holds
-// no rows: whatever lies there is left out), their maximum and their sum.
+// no rows: whatever lies there is left out), their maximum and their sum.  A piece whose keys
+// all weigh nothing has weight 0: its rows are 0, or the NaN that 0 times an infinity is.
 template <int Lanes>
 __device__ __forceinline__ void weigh(float e, float& m, float& w, float& total) {
-  m = e;
+  const bool none = e == kNoKeys;
+  m = none ? -INFINITY : e;
 #pragma unroll
   for (int k = 1; k < Lanes; k <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
-  w = e == -INFINITY ? -1.f : tc::exp2_fast(e - m);
+  w = none ? -1.f : e == -INFINITY ? 0.f : tc::exp2_fast(e - m);
   total = w < 0.f ? 0.f : w;
 #pragma unroll
   for (int k = 1; k < Lanes; k <<= 1) total += __shfl_xor_sync(0xffffffffu, total, k);
@@ -808,7 +854,7 @@ __device__ __forceinline__ void merge_few(const LatentArgs& a, const Merge& at, 
   constexpr int kRows = kMergeBatch / Span;
   const int column = quarter * 32 + lane;
   const bool mine = lane < kMergeBatch && lane % Span < u.pieces && row + lane / Span < u.rows;
-  const float e = mine ? at.log_sum(row + lane / Span, lane % Span) : -INFINITY;
+  const float e = mine ? at.log_sum(row + lane / Span, lane % Span) : kNoKeys;
   float4 x[kMergeBatch];
 #pragma unroll
   for (int k = 0; k < kMergeBatch; ++k) {
@@ -895,7 +941,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2)
     }
     const int row = nth / 4, quarter = nth % 4;
     auto piece_of = [&](int i) { return warp + i * kMergeWarps; };   // (32 at most a warp)
-    const float e = piece_of(lane) < u.pieces ? at.log_sum(row, piece_of(lane)) : -INFINITY;
+    const float e = piece_of(lane) < u.pieces ? at.log_sum(row, piece_of(lane)) : kNoKeys;
     float4 x[kMergeBatch], acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float m, w, total;
 #pragma unroll 1
