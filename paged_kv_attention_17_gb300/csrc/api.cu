@@ -3,6 +3,7 @@
 // Every entry point only enqueues work on the caller's stream: no allocation,
 // no synchronisation, no host read of device data.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <cudaTypedefs.h>
@@ -59,17 +60,17 @@ constexpr int kCascadeRows = 16;         // rows per tile of the cascade prefix 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 int device_sms(int device) {
-  static int cache[64] = {0};
+  static std::atomic<int> cache[64];               // (0: not asked for yet)
   if (device < 0 || device >= 64) return 0;
-  if (cache[device] == 0) {
-    int v = 0;
+  int v = cache[device].load(std::memory_order_relaxed);
+  if (v == 0) {
     if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) {
       cudaGetLastError();
       return 0;
     }
-    cache[device] = v;
+    cache[device].store(v, std::memory_order_relaxed);
   }
-  return cache[device];
+  return v;
 }
 
 int current_sms() {
@@ -84,16 +85,19 @@ int current_sms() {
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> known{nullptr};
+  PFN_cuTensorMapEncodeTiled_v12000 fn = known.load(std::memory_order_relaxed);
   if (fn == nullptr) {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
     if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
                                          &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
+        q == cudaDriverEntryPointSuccess) {
       fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    else
+      known.store(fn, std::memory_order_relaxed);
+    } else {
       cudaGetLastError();
+    }
   }
   return fn;
 }

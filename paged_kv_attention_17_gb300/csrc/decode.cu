@@ -53,6 +53,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "device_set.h"
 
 namespace pkv {
 
@@ -1980,11 +1981,11 @@ __global__ void __launch_bounds__(128) merge_rows_kernel(const AttnArgs a) {
 template <typename T, int D, int R, bool SPEC = false>
 static cudaError_t ensure_smem_attr() {
   using Sm = DecodeSmem<T, D, R>;
-  static unsigned done = 0;                 // one bit per device already configured
+  static DeviceSet done;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 32 && ((done >> dev) & 1u)) return cudaSuccess;
+  if (done.has(dev)) return cudaSuccess;
   e = cudaFuncSetAttribute(decode_kernel<T, D, R, SPEC>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, Sm::kAlloc);
   // the tensor-core build runs two CTAs per SM: ask for the largest
@@ -1992,7 +1993,7 @@ static cudaError_t ensure_smem_attr() {
   if (e == cudaSuccess && DecodeCfg<T, D, R>::kMma)
     e = cudaFuncSetAttribute(decode_kernel<T, D, R, SPEC>,
                              cudaFuncAttributePreferredSharedMemoryCarveout, 100);
-  if (e == cudaSuccess && dev < 32) done |= 1u << dev;
+  if (e == cudaSuccess) done.add(dev);
   return e;
 }
 

@@ -43,9 +43,9 @@
 // issue slots and 43% of the ALU pipe are taken (267 instructions a block and KV head:
 // 64 code conversions, 64 scale products, 17 MMAs).  One request of 8192 keys takes
 // 8.9 us: latency (metadata, table, first loads, 2 pairs a warp, merge, combine).
-#include <atomic>
 #include <cmath>
 
+#include "device_set.h"
 #include "e2m1.cuh"
 
 namespace pkv {
@@ -672,18 +672,18 @@ __global__ void __launch_bounds__(Cfg<D, NT, W>::kThreads, (Cfg<D, NT, W>::kCtas
 template <int D, int NT, int W>
 static cudaError_t launch_t(const AttnArgs& a, int row_tiles, cudaStream_t stream) {
   using C = Cfg<D, NT, W>;
-  static std::atomic<unsigned> done{0};                  // one bit per device already configured
+  static DeviceSet done;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev >= 32 || !((done >> dev) & 1u)) {
+  if (!done.has(dev)) {
     e = cudaFuncSetAttribute(decode_e2m1_kernel<D, NT, W>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(decode_e2m1_kernel<D, NT, W>,
                                cudaFuncAttributePreferredSharedMemoryCarveout, 100);
     if (e != cudaSuccess) return e;
-    if (dev < 32) done.fetch_or(1u << dev);
+    done.add(dev);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.hkv * a.num_splits),

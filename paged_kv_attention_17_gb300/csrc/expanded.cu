@@ -36,6 +36,7 @@
 // them take them at the end.
 #include <algorithm>
 
+#include "device_set.h"
 #include "latent.cuh"
 #include "tcgen05.cuh"
 
@@ -563,16 +564,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 cudaError_t launch_expanded(const ExpandedArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
                             const CUtensorMap& rmap, const CUtensorMap& vmap, int num_sms,
                             cudaStream_t stream) {
-  static unsigned done = 0;
+  static DeviceSet done;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev >= 32 || !((done >> dev) & 1u)) {
+  if (!done.has(dev)) {
     e = cudaFuncSetAttribute(expanded_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(expanded_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    if (dev < 32) done |= 1u << dev;
+    done.add(dev);
   }
   // (requests of 1 .. max_query_len tokens, num_tokens together)
   auto blocks = [&](int rows) {

@@ -49,6 +49,7 @@
 // 100 to 9000 keys, 128 heads, 101 us (0.64 PFLOP/s).
 #include <algorithm>
 
+#include "device_set.h"
 #include "latent.cuh"
 #include "latent_index.h"
 #include "tcgen05.cuh"
@@ -988,14 +989,14 @@ cudaError_t launch_latent(LatentArgs a, const CUtensorMap& qmap, const CUtensorM
   // (few rows: their partials lie close together, on few pages of memory)
   a.slot_rows = static_cast<int>(
       std::min<int64_t>(kUnitRows, static_cast<int64_t>(a.max_query_len) * a.hq));
-  static unsigned done = 0;
+  static DeviceSet done;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev >= 32 || !((done >> dev) & 1u)) {
+  if (!done.has(dev)) {
     e = cudaFuncSetAttribute(latent_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    if (dev < 32) done |= 1u << dev;
+    done.add(dev);
   }
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -75,6 +75,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "device_set.h"
 #include "e2m1.cuh"
 
 namespace pkv {
@@ -1118,16 +1119,16 @@ cudaError_t launch_prefill(const AttnArgs& a, const CUtensorMap& qmap, const CUt
                         prefill_kernel<128, kKvE4m3>, prefill_kernel<128, kKvE2m1>,
                         prefill_kernel<64, kKvE2m1>};
   const bool f8 = et != ElemType::kBf16;
-  static unsigned done = 0;
+  static DeviceSet done;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev >= 32 || !((done >> dev) & 1u)) {
+  if (!done.has(dev)) {
     for (int i = 0; i < 5 && e == cudaSuccess; ++i)
       e = cudaFuncSetAttribute(all[i], cudaFuncAttributeMaxDynamicSharedMemorySize,
                                smem_alloc(i >= 2));
     if (e != cudaSuccess) return e;
-    if (dev < 32) done |= 1u << dev;
+    done.add(dev);
   }
   // upper bound on the long requests' query tiles: sum ceil(n / 128) <=
   // ceil(N / 128) + (number of long requests); shared-prefix mode: pairs of
