@@ -102,14 +102,29 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
+// One tensor map.  The encoder is a driver call: it fails on a host thread that has no context
+// yet, such as a new one, while the runtime's calls bind the current device's by themselves.
+template <typename... Args>
+bool encode(Args... args) {
+  const auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  CUresult r = fn(args...);
+  if (r == CUDA_ERROR_INVALID_CONTEXT) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess)
+      r = fn(args...);
+    else
+      cudaGetLastError();
+  }
+  return r == CUDA_SUCCESS;
+}
+
 // 3-D map over one cache tensor viewed as [num_slots, num_kv_heads, head_dim]
 // (innermost first for TMA); a box covers 16 slots (one block) of one kv
 // head: the whole row unswizzled (decode kernel), or a 128-byte slice of it
 // with the 128B swizzle (prefill tensor-core operands).
 bool encode_cache_map(CUtensorMap* map, const void* base, int64_t num_slots, int hkv, int d,
                       ElemType et, bool swizzle128) {
-  auto fn = encode_fn();
-  if (fn == nullptr) return false;
   const cuuint64_t es = et == ElemType::kF32 ? 4 : (et == ElemType::kBf16 ? 2 : 1);
   const CUtensorMapDataType dt = et == ElemType::kF32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                  : et == ElemType::kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
@@ -120,11 +135,10 @@ bool encode_cache_map(CUtensorMap* map, const void* base, int64_t num_slots, int
   const cuuint32_t inner = swizzle128 ? static_cast<cuuint32_t>(128 / es) : static_cast<cuuint32_t>(d);
   cuuint32_t box[3] = {inner, 1, static_cast<cuuint32_t>(kBlock)};
   cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = fn(map, dt, 3,
+  return encode(map, dt, 3,
                   const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
 }
 
 // 4-D map for the tensor-core decode over a cache viewed as (column within a
@@ -135,8 +149,6 @@ bool encode_cache_map(CUtensorMap* map, const void* base, int64_t num_slots, int
 // row, the slice stride 128 bytes, the head stride one head's row.
 bool encode_slices_map(CUtensorMap* map, const void* base, int64_t num_slots, int hkv, int d,
                        ElemType et) {
-  auto fn = encode_fn();
-  if (fn == nullptr) return false;
   const cuuint64_t es = et == ElemType::kBf16 ? 2 : 1;
   const CUtensorMapDataType dt = et == ElemType::kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                        : CU_TENSOR_MAP_DATA_TYPE_UINT8;
@@ -148,10 +160,9 @@ bool encode_slices_map(CUtensorMap* map, const void* base, int64_t num_slots, in
   cuuint32_t box[4] = {static_cast<cuuint32_t>(128 / es), static_cast<cuuint32_t>(kBlock),
                        static_cast<cuuint32_t>(row / 128), 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
-  CUresult r = fn(map, dt, 4, const_cast<void*>(base), dims, strides, box, estr,
+  return encode(map, dt, 4, const_cast<void*>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
 }
 
 // The decode kernel's maps: rows of several 128-byte slices (bf16, D 128)
@@ -173,26 +184,21 @@ bool encode_decode_maps(CUtensorMap* kmap, CUtensorMap* vmap, const void* k_cach
 // of the group's heads), 64 columns wide (128 bytes, 128B swizzle).
 bool encode_q_map(CUtensorMap* map, const void* q, int64_t num_tokens, int hq, int d,
                   int heads_per_box = 1) {
-  auto fn = encode_fn();
-  if (fn == nullptr) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(hq),
                         static_cast<cuuint64_t>(num_tokens)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(hq) * d * 2};
   cuuint32_t box[3] = {64, static_cast<cuuint32_t>(heads_per_box),
                        static_cast<cuuint32_t>(128 / heads_per_box)};
   cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides,
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides,
                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
 }
 
 // Maps over bf16 rows of `cols` elements `stride` elements apart, in boxes of 64 columns (128
 // bytes, 128B swizzle) by `box_rows` rows; with heads, head_stride apart, of one head.
 bool encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, int cols, int64_t stride,
                      int box_rows, int heads = 0, int64_t head_stride = 0) {
-  auto fn = encode_fn();
-  if (fn == nullptr) return false;
   const cuuint64_t r = static_cast<cuuint64_t>(rows), c = static_cast<cuuint64_t>(cols);
   const cuuint64_t row_bytes = static_cast<cuuint64_t>(stride) * 2;
   const cuuint32_t n = static_cast<cuuint32_t>(box_rows);
@@ -201,25 +207,23 @@ bool encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, int cols,
       heads > 0 ? static_cast<cuuint64_t>(head_stride) * 2 : row_bytes, row_bytes};
   const cuuint32_t box[3] = {64, heads > 0 ? 1 : n, n};
   const cuuint32_t estr[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, heads > 0 ? 3 : 2, const_cast<void*>(base), dims,
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, heads > 0 ? 3 : 2, const_cast<void*>(base), dims,
             strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // 3-D map over a latent cache viewed as (column within a 128-byte slab, slot, slab): a box
 // is every slab of 8 slots' rows, landing [slab][8 rows][128 bytes] (128B swizzle).
 bool encode_latent_map(CUtensorMap* map, const void* base, int64_t num_slots) {
-  auto fn = encode_fn();
-  if (fn == nullptr) return false;
   cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(num_slots), kLatentRow / 64};
   cuuint64_t strides[2] = {kLatentRow * 2, 128};
   cuuint32_t box[3] = {64, 8, kLatentRow / 64};
   cuuint32_t estr[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 bool valid_dtype(pkv_dtype dt) { return dt == PKV_F32 || dt == PKV_BF16; }
