@@ -367,7 +367,7 @@ pkv_status pkv_latent_attention_varlen(const void* q, const void* cache, void* o
  * Runs on tcgen05 tensor cores, P rounded to bf16 for its product.  What rows other than
  * a request's own keys hold never reaches its rows, nor a later key one that does not see
  * it; infinities and NaN that a row sees reach it.  num_q_heads <= 4096, num_seqs <= 65535,
- * num_tokens * num_q_heads and num_keys < 2^31 (else PKV_ERR_UNSUPPORTED).
+ * num_tokens * num_q_heads < 2^31 and num_keys <= 2^30 (else PKV_ERR_UNSUPPORTED).
  */
 pkv_status pkv_expanded_attention_varlen(const void* q, const pkv_rows* k,
                                          const pkv_rows* k_rope, const pkv_rows* v, void* out,

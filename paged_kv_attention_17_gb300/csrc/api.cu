@@ -841,7 +841,8 @@ pkv_status pkv_expanded_attention_varlen(const void* q, const pkv_rows* k, const
   if (num_seqs < 0 || num_tokens < 0 || num_keys < 0 || num_q_heads < 1 || max_query_len < 0 ||
       max_key_len < 0 || !std::isfinite(softmax_scale))
     return PKV_ERR_INVALID_ARG;
-  if (softmax_scale <= 0.f || num_seqs > 65535 || num_q_heads > 4096 || num_keys > 0x7FFFFFFFll ||
+  // (2^30 keys: the last tile's end, past a request's keys, stays in 32 bits)
+  if (softmax_scale <= 0.f || num_seqs > 65535 || num_q_heads > 4096 || num_keys > (1ll << 30) ||
       num_tokens > 0x7FFFFFFFll / num_q_heads)
     return PKV_ERR_UNSUPPORTED;
   if (num_seqs == 0 || num_tokens == 0) return PKV_OK;
