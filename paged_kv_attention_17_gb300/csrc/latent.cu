@@ -119,14 +119,15 @@ __host__ __device__ inline Layout layout(int blocks) {
 __device__ __forceinline__ int lse_at(int row, int slot, int blocks) { return row * 2 * blocks + slot; }
 
 // mbar_wait by polling: the suspended wait wakes up some hundred cycles late.
-__device__ __forceinline__ bool poll(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool poll(uint64_t* bar, uint32_t parity,
+                                     unsigned long long limit_ns = kWaitLimitNs) {
   unsigned long long t0 = 0;
   for (uint32_t i = 0;; ++i) {
     if (mbar_ready(bar, parity)) return true;
     if ((i & 255) == 255) {
       const unsigned long long t = globaltimer();
       if (t0 == 0) t0 = t;
-      else if (t - t0 > kWaitLimitNs) return false;
+      else if (t - t0 > limit_ns) return false;
     }
   }
 }
@@ -324,6 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         x = start->request;
       }
       uint32_t units = 0;
+      int tiles = 0;                             // of the piece whose queries are loaded
       for (uint32_t k = 0; ok; ++k) {
         bool more = w.next(x, p);
         while (!more && w.v < w.end && r + 1 < a.num_seqs) {
@@ -353,8 +355,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&job_full[k % kJobs]);
         if (!more) break;
         if (p.tile0 >= p.tile1) continue;
-        if (units > 0) ok = poll(q_empty, (units - 1) & 1);
+        // (this one wait is as long as a piece)
+        if (units > 0) ok = poll(q_empty, (units - 1) & 1, kWaitLimitNs + piece_limit_ns(tiles));
         if (!ok) break;
+        tiles = p.tile1 - p.tile0;
         mbar_arrive_expect_tx(q_full, kQueries);
         for (int s = 0; s < kSlabs; ++s)
           tc::load_2d(smem + s * kSlab, &qmap, q_full, s * 64, j.row0, policy);

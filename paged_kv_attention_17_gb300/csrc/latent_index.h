@@ -127,6 +127,10 @@ PKV_LATENT_INDEX Page page_of(int b, int blocks, int entry, int64_t num_blocks) 
   return entry >= 0 && entry < num_blocks ? Page::kLoad : Page::kBad;
 }
 
+// Time, beyond a single wait's, that a piece of so many tiles may take at most: a tile takes 1.0
+// to 2.0 us as it streams, and this allows ten times that.
+PKV_LATENT_INDEX uint64_t piece_limit_ns(int tiles) { return static_cast<uint64_t>(tiles) * 20000; }
+
 // Partials: block c keeps the piece that begins inside a unit in slot 2 c, the piece that
 // a later block goes on with in slot 2 c + 1.
 PKV_LATENT_INDEX int piece_slot(int block, bool first) { return 2 * block + (first ? 1 : 0); }
