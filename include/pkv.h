@@ -107,7 +107,7 @@ typedef enum { PKV_F32 = 0, PKV_BF16 = 1 } pkv_dtype;
  *   k_cache, v_cache  device, [num_blocks, block_size, num_kv_heads, head_dim].
  *   error_flag     device int32 or NULL.
  * Slots not named by slot_mapping keep their contents.  Two tokens naming
- * the same slot leave either one's row there (unspecified which).
+ * the same slot leave its contents unspecified (parts of either's rows).
  * num_tokens == 0 is a no-op returning PKV_OK.
  */
 pkv_status pkv_write(const void* k_new, const void* v_new, const int64_t* slot_mapping,
@@ -240,7 +240,8 @@ typedef struct {
  *                  with num_q_heads == 0: keys only.
  *   k_new, v_new   [num_tokens, num_kv_heads, head_dim], dtype.
  *   head_dim       a multiple of 16.
- * A padding token's q (negative slot) is turned too.  Everything else as pkv_write.
+ * A padding token's q (negative slot) is turned too.  Everything else as pkv_write: two
+ * tokens naming the same slot leave its contents unspecified, here and in the forms below.
  */
 pkv_status pkv_rotate_write(const pkv_rotation* rotation, const pkv_rows* q,
                             const pkv_rows* q_out, const pkv_rows* k_new, const pkv_rows* v_new,
@@ -331,9 +332,11 @@ size_t pkv_latent_workspace_bytes(int device);
  * What a row does not see never reaches it.  A row that sees a NaN or +inf score is NaN.  A
  * score of -inf weighs 0: where such a key holds an infinity, that element of the rows that
  * see it is NaN (0 times it); a row with no other scores is 0 elsewhere, its log-sum-exp
- * -inf.  num_q_heads <= 4096, num_seqs <= 65535, num_tokens * num_q_heads and num_blocks
- * * 16 < 2^31 (else PKV_ERR_UNSUPPORTED); a context is at most 2^30 keys.  The rest as
- * pkv_attention_varlen.
+ * -inf.  Sums of weighted values are fp32, and tensor cores cut them off: with all weights and
+ * signs alike an element is short by 1e-4 of itself where an SM takes 2^18 keys of a request,
+ * 2e-3 for 2^20, 1.5e-2 for 2^22.  num_q_heads <= 4096, num_seqs <= 65535, num_tokens *
+ * num_q_heads and num_blocks * 16 < 2^31 (else PKV_ERR_UNSUPPORTED); a context is at most 2^30
+ * keys.  The rest as pkv_attention_varlen.
  */
 pkv_status pkv_latent_attention_varlen(const void* q, const void* cache, void* out,
                                        float* lse_out, const int32_t* query_start_loc,
@@ -366,8 +369,11 @@ pkv_status pkv_latent_attention_varlen(const void* q, const void* cache, void* o
  *   softmax_scale  finite, > 0 (else PKV_ERR_UNSUPPORTED).
  * Runs on tcgen05 tensor cores, P rounded to bf16 for its product.  What rows other than
  * a request's own keys hold never reaches its rows, nor a later key one that does not see
- * it; infinities and NaN that a row sees reach it.  num_q_heads <= 4096, num_seqs <= 65535,
- * num_tokens * num_q_heads < 2^31 and num_keys <= 2^30 (else PKV_ERR_UNSUPPORTED).
+ * it; infinities and NaN that a row sees reach it (an infinity whose weight rounds to 0 as
+ * itself or as a NaN).  Where query_start_loc decreases, any row may be left unwritten.  Sums
+ * are cut off as in the absorbed form, over all of a request's keys.  num_q_heads <= 4096,
+ * num_seqs <= 65535, num_tokens * num_q_heads < 2^31 and num_keys <= 2^30 (else
+ * PKV_ERR_UNSUPPORTED).
  */
 pkv_status pkv_expanded_attention_varlen(const void* q, const pkv_rows* k,
                                          const pkv_rows* k_rope, const pkv_rows* v, void* out,

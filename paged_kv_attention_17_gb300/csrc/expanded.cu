@@ -22,8 +22,10 @@
 // MMAs for both query tiles (12 of 192 / 16 steps and 8 of 128 / 16, 64 cycles each) and 2048
 // of exponentials; it takes about 3500, which is a tile's chain from scores through softmax and
 // P V to the next scores: P lies over its own S, as TMEM has no room beside two S and two O.
-// Measured: 8192 tokens of 32 heads, causal, in 500 us, 1.37 PFLOP/s (72% of a library matrix
-// product's rate); five prompts of 130 to 777 tokens on up to 333 cached, 12 heads, 23 us.
+// Measured: 8192 tokens of 32 heads, causal, in 500 us (498 to 514 from card to card), 1.37
+// PFLOP/s (72% of a library matrix product's rate; the tensor pipe is busy for 62% of the time, with
+// the units' starts, their ends and the tiles that the causal limit crosses); five prompts of 130
+// to 777 tokens on up to 333 cached, 12 heads, 23 us.
 // Tried and slower: P handed on in two halves (519 us for the 8192 tokens: the second wait and
 // store cost the softmax warps more than the earlier product gives), an eighth or a quarter
 // of the exponentials as polynomials on the FMA units (517, 561 us: the warps' instructions

@@ -40,12 +40,14 @@
 //
 // What bounds it.  HBM where a key meets few rows; from about 64 rows a key, shared memory: a
 // tile of 64 keys and 64 rows is 36 MMAs that read 4 KB each and 16 that read 6 KB, beside 72
-// KB that the copy engine writes, 2500 cycles at 128 bytes a cycle; it takes about 2900.  (A
-// tile of 128 rows would halve the reads a row, but its queries leave no room for two stages
-// of keys.)  Few tiles a block: the way to the first scores, 6 us (lengths, table and keys
+// KB that the copy engine writes, 2500 cycles at 128 bytes a cycle; it takes about 2900.
+// (Counted, of all active cycles of the 16 requests below, start and end among them: the tensor
+// cores read shared memory in 53%, the warps use it in 6%; the copy engine's bytes are another
+// 16%.  A tile of 128 rows would halve the reads a row, but its queries leave no room for
+// two stages of keys.)  Few tiles a block: the way to the first scores, 6 us (lengths, table and keys
 // are fetched one after the other), and the merge's launch and its fetch, 5 us.
-// Measured: 1 request of 8192 keys, 16 heads, 14.2 us; 64 of 512 to 4096 keys, 32 heads, 43 us
-// (153 MB, 3.6 TB/s); 2 of 131000, 64 heads, 68 us (302 MB, 4.4 TB/s); 16 of three tokens and
+// Measured: 1 request of 8192 keys, 16 heads, 14.3 us; 64 of 512 to 4096 keys, 32 heads, 43.3 us
+// (153 MB, 3.5 TB/s); 2 of 131000, 64 heads, 69 us (302 MB, 4.4 TB/s); 16 of three tokens and
 // 100 to 9000 keys, 128 heads, 101 us (0.64 PFLOP/s).
 #include <algorithm>
 
@@ -91,8 +93,10 @@ constexpr int kTmemCols = 512;
 constexpr int kColO = 0, kColS = 256;
 constexpr float kSlack = 8.f;
 constexpr float kNoKeys = INFINITY;              // for the log-sum-exps of a piece without tiles
-// Tiles a block takes at least.  1 request of 8192 keys: 15.1 us with 1 (more pieces to
-// merge), 14.2 with 2, 15.3 with 3, 15.8 with 4.
+// Tiles a block takes at least (it matters where there are few).  With 1 (more pieces to merge),
+// 2, 3 and 4, in us: 1 request of 1000 keys, 16 heads, 12.4, 12.4, 14.8, 15.4; of 8192 keys 15.0,
+// 14.8, 15.7, 16.3, with 128 heads 18.8, 18.8, 20.3, 20.6; of 40000 keys 23.1, 22.9, 23.1, 23.0;
+// 4 of 4000 keys 15.6, 15.6, 17.1, 17.6; 8 of 300 to 2000, 32 heads, 18.7, 18.7, 17.2, 17.7.
 constexpr int kLeastPositions = 2;
 constexpr int kMergeThreads = 256, kMergeWarps = kMergeThreads / 32;
 constexpr int kMergeBatch = 16;                  // pieces a thread has in flight

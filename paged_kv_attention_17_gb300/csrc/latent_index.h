@@ -23,9 +23,11 @@ namespace pkv {
 
 constexpr int kUnitRows = 64;                    // rows of a unit
 constexpr int kTileKeys = 64;                    // keys of a tile
-// Tiles that a unit's start and end take as long as.  16 requests of 6 units each: 108.4 us
-// with 1, 104.6 with 2, 101.4 with 3, 103.4 with 4, 104.6 with 6; 64 requests of one unit:
-// 43.0, 42.6, 43.0, 43.3, 44.6.
+// Tiles that a unit's start and end take as long as.  With 1, 2, 3, 4 and 6, in us: 16 requests of 6
+// units on 100 to 9000 keys 104.6, 99.0, 97.5, 100.4, 101.8; 32 requests of 2 units on 200 to 3000
+// keys 44.4, 39.9, 41.2, 42.0, 43.2; 256 requests of one unit on 200 to 900 keys 47.9, 48.2, 49.2,
+// 50.6, 52.8; 64 on 512 to 4096 keys 48.5, 48.4, 48.6, 49.0, 50.3; 4 requests of 75 units 106.6 with
+// any.  2 and 3 are within 3% of each other everywhere; 3 does better where it saves most.
 constexpr int kUnitCost = 3;
 
 // a / b (b > 0) by a 32-bit division where that will do: the 64-bit one is a long call.
